@@ -54,7 +54,9 @@ typedef enum svd_status {
     SVD_ERR_CUDA = 4,          /* a CUDA runtime call or launch failed */
     SVD_ERR_TIMEOUT = 5,       /* device: a bounded wait ran out (status word only) */
     SVD_ERR_UNSUPPORTED = 6,   /* shape outside the supported range (e.g. V too large) */
-    SVD_ERR_TOKEN_RANGE = 7    /* device: a caller draft token outside [0, V) (status word) */
+    SVD_ERR_TOKEN_RANGE = 7,   /* device: a caller draft token outside [0, V) (status word) */
+    SVD_ERR_PAGE_RANGE = 8,    /* device: a page id or cache length out of range (status word) */
+    SVD_ERR_TREE = 9           /* device: a parent or a path's node out of range (status word) */
 } svd_status;
 
 typedef enum svd_mode {
@@ -281,8 +283,8 @@ svd_status svd_speedup_report(const int32_t* accept_len, const int32_t* bk,
                               void* stream);
 
 /* Reads and clears the device status word of `ws` (synchronizes `stream`).  Returns SVD_OK,
- * SVD_ERR_TOKEN_RANGE or SVD_ERR_TIMEOUT as recorded by kernels that used this workspace, or
- * SVD_ERR_CUDA if the read itself failed. */
+ * SVD_ERR_TOKEN_RANGE, SVD_ERR_TIMEOUT, SVD_ERR_PAGE_RANGE or SVD_ERR_TREE as recorded by kernels
+ * that used this workspace, or SVD_ERR_CUDA if the read itself failed. */
 svd_status svd_get_device_error(void* ws, void* stream);
 
 /* Human-readable name of a status code (static storage). */

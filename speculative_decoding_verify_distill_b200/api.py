@@ -20,7 +20,8 @@ LIB_PATH = os.path.join(_PKG, "libsvd.so")
 SVD_OK = 0
 STATUS_NAMES = {0: "SVD_OK", 1: "SVD_ERR_INVALID_ARG", 2: "SVD_ERR_ALIGNMENT",
                 3: "SVD_ERR_WORKSPACE", 4: "SVD_ERR_CUDA", 5: "SVD_ERR_TIMEOUT",
-                6: "SVD_ERR_UNSUPPORTED", 7: "SVD_ERR_TOKEN_RANGE"}
+                6: "SVD_ERR_UNSUPPORTED", 7: "SVD_ERR_TOKEN_RANGE", 8: "SVD_ERR_PAGE_RANGE",
+                9: "SVD_ERR_TREE"}
 GREEDY, STOCHASTIC = 0, 1
 BK_CEIL, BK_FLOOR = 0, 1
 
@@ -79,6 +80,50 @@ class VsArgs(ctypes.Structure):
     ]
 
 
+_I64 = ctypes.c_int64
+
+
+class TreeAttentionArgs(ctypes.Structure):
+    """Mirror of ``svd_tree_attention_args`` (include/svd_tree.h)."""
+    _fields_ = [
+        ("q", _P), ("k_new", _P), ("v_new", _P), ("cache_k", _P), ("cache_v", _P),
+        ("page_stride_k", _I64), ("page_stride_v", _I64), ("page_table", _P), ("cache_len", _P),
+        ("parent", _P), ("n_nodes", _P), ("B", _I), ("n", _I), ("Hq", _I), ("Hkv", _I), ("D", _I),
+        ("n_pages", _I), ("page_size", _I), ("max_pages", _I), ("dtype", _I), ("scale", _F),
+        ("out", _P), ("lse", _P),
+    ]
+
+
+class LogitsProcessArgs(ctypes.Structure):
+    """Mirror of ``svd_logits_process_args``."""
+    _fields_ = [
+        ("logits", _P), ("B", _I), ("n", _I), ("V", _I), ("history", _P), ("hist_stride", _I),
+        ("prompt_len", _P), ("hist_len", _P), ("node_tok", _P), ("parent", _P),
+        ("repetition", _P), ("frequency", _P), ("presence", _P), ("bias_tok", _P), ("bias_val", _P),
+        ("n_bias", _I), ("mask", _P), ("mask_rows", _I), ("mask_value", _F), ("out", _P),
+        ("argmax", _P), ("dz", _P), ("dlogits", _P), ("grad_fp32", _I),
+    ]
+
+
+class TreeVerifyArgs(ctypes.Structure):
+    """Mirror of ``svd_tree_verify_args``."""
+    _fields_ = [
+        ("T", _P), ("target_tok", _P), ("node_tok", _P), ("parent", _P), ("n_nodes", _P),
+        ("B", _I), ("n", _I), ("V", _I), ("target_argmax", _P), ("path", _P), ("n_path", _P),
+        ("accept_len", _P), ("emitted", _P), ("n_emitted", _P),
+    ]
+
+
+class CacheAppendArgs(ctypes.Structure):
+    """Mirror of ``svd_cache_append_args``."""
+    _fields_ = [
+        ("k_new", _P), ("v_new", _P), ("cache_k", _P), ("cache_v", _P), ("page_stride_k", _I64),
+        ("page_stride_v", _I64), ("page_table", _P), ("cache_len", _P), ("count", _P), ("path", _P),
+        ("B", _I), ("n", _I), ("Hkv", _I), ("D", _I), ("n_pages", _I), ("page_size", _I),
+        ("max_pages", _I), ("new_len", _P),
+    ]
+
+
 _lib = None
 
 
@@ -114,6 +159,17 @@ def lib():
     L.svd_vs_stats.argtypes = [ctypes.POINTER(VsArgs), _P, _P, _SZ, _P]
     L.svd_vs_resolve.argtypes = [ctypes.POINTER(VsArgs), _P, _P, _P, _SZ, _P]
     L.svd_vs_finish.argtypes = [ctypes.POINTER(VsArgs), _P, _P, _SZ, _P]
+    L.svd_tree_attention_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
+    L.svd_logits_process_workspace_bytes.argtypes = [_I, _I]
+    L.svd_tree_verify_workspace_bytes.argtypes = [_I, _I]
+    L.svd_cache_append_workspace_bytes.argtypes = [_I]
+    for fn in ("svd_tree_attention", "svd_logits_process", "svd_tree_verify", "svd_cache_append"):
+        getattr(L, fn + "_workspace_bytes").restype = _SZ
+    for fn, args in (("svd_tree_attention", TreeAttentionArgs), ("svd_logits_process", LogitsProcessArgs),
+                     ("svd_logits_process_grad", LogitsProcessArgs), ("svd_tree_verify", TreeVerifyArgs),
+                     ("svd_cache_append", CacheAppendArgs)):
+        getattr(L, fn).argtypes = [ctypes.POINTER(args), _P, _SZ, _P]
+        getattr(L, fn).restype = _I
     for fn in ("svd_workspace_reset", "svd_length_head", "svd_verify", "svd_distill_loss_grad",
                "svd_verify_distill", "svd_get_device_error", "svd_selftest_wait_timeout",
                "svd_verify_distill_noalloc", "svd_speedup_report", "svd_length_head_update",
@@ -545,3 +601,338 @@ class VocabShard:
         if self.row_info is not None:
             out["row_info"] = self.row_info
         return out
+
+
+# ------------------------------------------------------------------------------------------
+# operators on a tree of drafts (include/svd_tree.h)
+# ------------------------------------------------------------------------------------------
+TREE_MAX_NODES = 64
+MASK_VALUE = -32768.0   # finite: svd_verify and svd_verify_distill want finite logits
+
+
+def _tensor(t, name: str, dtype, shape, dev):
+    """Pointer of a contiguous CUDA tensor with this dtype (or one of them) and shape; None passes."""
+    if t is None:
+        return None
+    p = _ptr(t)
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError("%s: unexpected dtype %s" % (name, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != dev:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    return p
+
+
+def _pages(t, name: str, dtype, like, dev):
+    """Pointer and page stride of a cache [n_pages, page_size, Hkv, D]; pages may lie apart (a slice
+    of a buffer that holds K and V pages), their inside is contiguous."""
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.dtype != dtype or t.device != dev:
+        raise TypeError("%s must be %s on %s, got %s on %s" % (name, dtype, dev, t.dtype, t.device))
+    if t.dim() != 4 or tuple(t.shape[2:]) != tuple(like):
+        raise ValueError("%s must be [n_pages, page_size, %d, %d], got %s" % ((name,) + tuple(like) + (tuple(t.shape),)))
+    if t.shape[0] and not t[0].is_contiguous():
+        raise ValueError("%s: the inside of a page must be contiguous" % name)
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2] * t.shape[3]
+    return ctypes.c_void_p(t.data_ptr()), stride
+
+
+class _TreeOp:
+    """Preallocated outputs, argument block and workspace of one operator, for repeated calls.
+
+    The calls of one object share its workspace and outputs: a call on another stream than the
+    last one first waits for that stream (not while it is being captured: order captured calls
+    yourself, and give graphs that may run at the same time an object each)."""
+
+    _fn = ""
+
+    def _set_up(self, args, nbytes: int, dev, keep):
+        self.args, self.device, self._keep = args, dev, keep
+        with torch.cuda.device(dev):
+            self.ws = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+            self._last = torch.cuda.current_stream(dev)
+        assert self.ws.data_ptr() % 256 == 0
+        self._call = getattr(lib(), self._fn)
+        self._ws = (ctypes.c_void_p(self.ws.data_ptr()), self.ws.numel())
+        self._ref = ctypes.byref(args)
+
+    def _order(self, s):
+        if s.device != self.device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (s.device, self.device))
+        with torch.cuda.stream(s):
+            capturing = torch.cuda.is_current_stream_capturing()
+        if not capturing:
+            s.wait_stream(self._last)
+            for t in [self.ws, *self.outputs().values()]:
+                t.record_stream(s)
+            self._last = s
+
+    def __call__(self, stream=None):
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        if s.cuda_stream != self._last.cuda_stream or s.device != self.device:
+            self._order(s)
+        if torch.cuda.current_device() == self.device.index:
+            _check(self._call(self._ref, *self._ws, s.cuda_stream), self._fn)
+        else:
+            with torch.cuda.device(self.device):
+                _check(self._call(self._ref, *self._ws, s.cuda_stream), self._fn)
+        return self
+
+    def device_error(self, stream=None) -> int:
+        """The status word of the calls so far (synchronizes)."""
+        with torch.cuda.device(self.device):
+            s = self._last if stream is None else stream
+            return int(lib().svd_get_device_error(self._ws[0], s.cuda_stream))
+
+
+def _once(op, args, kw, stream):
+    """One call of a fresh object, with its buffers allocated on the stream that it runs on."""
+    if stream is None:
+        return op(*args, **kw)().outputs()
+    with torch.cuda.stream(stream):
+        return op(*args, **kw)(stream).outputs()
+
+
+class TreeAttention(_TreeOp):
+    """Attention of the drafted nodes over the paged cache and over their ancestors.
+
+    ``q`` [B, n, Hq, D], ``k_new`` and ``v_new`` [B, n, Hkv, D], ``cache_k`` and ``cache_v``
+    [n_pages, page_size, Hkv, D], all bf16 or all fp16; ``page_table`` [B, max_pages] and
+    ``cache_len`` [B] int32.  ``parent`` [B, n] int32 gives the tree (default: a chain), ``n_nodes``
+    [B] int32 the nodes in use.  ``n = 1`` is a decode step.  Outputs: ``out`` [B, n, Hq, D] and,
+    with ``lse=True``, ``lse`` [B, n, Hq] fp32."""
+
+    _fn = "svd_tree_attention"
+
+    def __init__(self, q, k_new, v_new, cache_k, cache_v, page_table, cache_len, *, parent=None,
+                 n_nodes=None, scale: Optional[float] = None, lse: bool = False):
+        if q.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("expected bf16 or fp16 queries, got %s" % q.dtype)
+        if q.dim() != 4 or k_new.dim() != 4:
+            raise ValueError("q is [B, n, Hq, D], k_new and v_new are [B, n, Hkv, D]")
+        B, n, Hq, D = q.shape
+        Hkv, dev, i32 = k_new.shape[2], q.device, torch.int32
+        a = TreeAttentionArgs()
+        a.q = _tensor(q, "q", q.dtype, q.shape, dev)
+        a.k_new = _tensor(k_new, "k_new", q.dtype, (B, n, Hkv, D), dev)
+        a.v_new = _tensor(v_new, "v_new", q.dtype, (B, n, Hkv, D), dev)
+        a.cache_k, a.page_stride_k = _pages(cache_k, "cache_k", q.dtype, (Hkv, D), dev)
+        a.cache_v, a.page_stride_v = _pages(cache_v, "cache_v", q.dtype, (Hkv, D), dev)
+        if cache_k.shape != cache_v.shape:
+            raise ValueError("cache_k and cache_v differ in shape")
+        a.n_pages, a.page_size, a.max_pages = cache_k.shape[0], cache_k.shape[1], page_table.shape[-1]
+        a.page_table = _tensor(page_table, "page_table", i32, (B, a.max_pages), dev)
+        a.cache_len = _tensor(cache_len, "cache_len", i32, (B,), dev)
+        a.parent = _tensor(parent, "parent", i32, (B, n), dev)
+        a.n_nodes = _tensor(n_nodes, "n_nodes", i32, (B,), dev)
+        a.B, a.n, a.Hq, a.Hkv, a.D = B, n, Hq, Hkv, D
+        a.dtype = 0 if q.dtype == torch.bfloat16 else 1
+        a.scale = float(1.0 / math.sqrt(max(D, 1)) if scale is None else scale)
+        self.out = torch.empty_like(q)
+        self.lse = torch.empty((B, n, Hq), dtype=torch.float32, device=dev) if lse else None
+        a.out, a.lse = _ptr(self.out), _ptr(self.lse)
+        self._set_up(a, lib().svd_tree_attention_workspace_bytes(B, n, Hq, Hkv, D), dev,
+                     [q, k_new, v_new, cache_k, cache_v, page_table, cache_len, parent, n_nodes])
+
+    def outputs(self) -> dict:
+        return dict(out=self.out) if self.lse is None else dict(out=self.out, lse=self.lse)
+
+
+def svd_tree_attention(*args, stream=None, **kw) -> dict:
+    """One call; arguments as in :class:`TreeAttention`."""
+    return _once(TreeAttention, args, kw, stream)
+
+
+def _lists(a, logits, history, prompt_len, hist_len, node_tok, parent, repetition, mask):
+    """The arguments that the processing and its gradient share."""
+    if logits.dim() != 3:
+        raise ValueError("logits are [B, n, V]")
+    B, n, V = logits.shape
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    a.logits = _ptr(_bits(logits))
+    a.B, a.n, a.V = B, n, V
+    if history is None and (prompt_len is not None or hist_len is not None):
+        raise ValueError("prompt_len and hist_len go with history")
+    if history is not None:
+        a.hist_stride = history.shape[-1]
+        a.history = _tensor(history, "history", i32, (B, a.hist_stride), dev)
+    a.prompt_len = _tensor(prompt_len, "prompt_len", i32, (B,), dev)
+    a.hist_len = _tensor(hist_len, "hist_len", i32, (B,), dev)
+    a.node_tok = _tensor(node_tok, "node_tok", i32, (B, n), dev)
+    a.parent = _tensor(parent, "parent", i32, (B, n), dev)
+    a.repetition = _tensor(repetition, "repetition", f32, (B,), dev)
+    if mask is not None:
+        if mask.dim() != 3 or mask.shape[1] not in (1, n):
+            raise ValueError("mask is [B, 1 or n, ceil(V / 32)]")
+        a.mask_rows = mask.shape[1]
+        a.mask = _tensor(mask, "mask", (i32, torch.uint32), (B, a.mask_rows, (V + 31) // 32), dev)
+
+
+class LogitsProcess(_TreeOp):
+    """Penalties, biases and grammar masks on the logits [B, n, V] of every row of a tree.
+
+    ``history`` [B, S] int32 holds a sequence's tokens: ``prompt_len`` [B] of the prompt, then the
+    generated ones up to ``hist_len`` [B]; ``node_tok`` [B, n] and ``parent`` [B, n] the drafted
+    ones, of which a row sees its ancestors' and its own.  ``repetition``, ``frequency`` and
+    ``presence`` [B] fp32; ``bias_tok`` [B, nb] int32 with ``bias_val`` [B, nb] fp32; ``mask``
+    [B, 1 or n, ceil(V / 32)] int32, a set bit allows the id, the others get ``mask_value``.
+    -1 in a list of ids is padding.  ``out`` may be ``logits`` (in place).  Outputs: ``out`` bf16
+    (unless ``values=False``) and, with ``argmax=True``, ``argmax`` [B, n] int32 of the result."""
+
+    _fn = "svd_logits_process"
+
+    def __init__(self, logits, *, history=None, prompt_len=None, hist_len=None, node_tok=None,
+                 parent=None, repetition=None, frequency=None, presence=None, bias_tok=None,
+                 bias_val=None, mask=None, mask_value: float = MASK_VALUE, out=None,
+                 values: bool = True, argmax: bool = False):
+        a = LogitsProcessArgs()
+        _lists(a, logits, history, prompt_len, hist_len, node_tok, parent, repetition, mask)
+        B, n, V = logits.shape
+        dev, i32, f32 = logits.device, torch.int32, torch.float32
+        a.frequency = _tensor(frequency, "frequency", f32, (B,), dev)
+        a.presence = _tensor(presence, "presence", f32, (B,), dev)
+        if (bias_tok is None) != (bias_val is None):
+            raise ValueError("bias_tok and bias_val go together")
+        if bias_tok is not None:
+            a.n_bias = bias_tok.shape[-1]
+            a.bias_tok = _tensor(bias_tok, "bias_tok", i32, (B, a.n_bias), dev)
+            a.bias_val = _tensor(bias_val, "bias_val", f32, (B, a.n_bias), dev)
+        a.mask_value = float(mask_value)
+        if not values and (out is not None or not argmax):
+            raise ValueError("values=False leaves argmax=True alone, without out")
+        self.out = (torch.empty_like(logits) if out is None else out) if values else None
+        self.argmax = torch.empty((B, n), dtype=i32, device=dev) if argmax else None
+        a.out = _tensor(self.out, "out", torch.bfloat16, (B, n, V), dev)
+        a.argmax = _ptr(self.argmax)
+        self._set_up(a, lib().svd_logits_process_workspace_bytes(B, n), dev,
+                     [logits, history, prompt_len, hist_len, node_tok, parent, repetition, frequency,
+                      presence, bias_tok, bias_val, mask])
+
+    def outputs(self) -> dict:
+        return {k: t for k, t in (("out", self.out), ("argmax", self.argmax)) if t is not None}
+
+
+def svd_logits_process(logits, stream=None, **kw) -> dict:
+    """One call; arguments as in :class:`LogitsProcess`."""
+    return _once(LogitsProcess, (logits,), kw, stream)
+
+
+class LogitsProcessGrad(_TreeOp):
+    """Gradient of :class:`LogitsProcess` with respect to the raw ``logits``, from the gradient ``dz``
+    [B, n, V] (bf16 or fp32) with respect to its output, e.g. ``dlogits`` of :class:`VerifyDistill`
+    on processed logits.  ``out`` may be ``dz`` (in place).  Frequency, presence and bias shift a
+    logit and do not appear.  Output: ``dlogits`` of dz's type."""
+
+    _fn = "svd_logits_process_grad"
+
+    def __init__(self, dz, logits, *, history=None, prompt_len=None, hist_len=None, node_tok=None,
+                 parent=None, repetition=None, frequency=None, presence=None, bias_tok=None,
+                 bias_val=None, mask=None, out=None):
+        a = LogitsProcessArgs()
+        _lists(a, logits, history, prompt_len, hist_len, node_tok, parent, repetition, mask)
+        B, n, V = logits.shape
+        dev = logits.device
+        a.dz = _tensor(dz, "dz", (torch.bfloat16, torch.float32), (B, n, V), dev)
+        self.dlogits = torch.empty_like(dz) if out is None else out
+        a.dlogits = _tensor(self.dlogits, "out", dz.dtype, (B, n, V), dev)
+        a.grad_fp32 = int(dz.dtype == torch.float32)
+        self._set_up(a, lib().svd_logits_process_workspace_bytes(B, n), dev,
+                     [dz, logits, history, prompt_len, hist_len, node_tok, parent, repetition, mask])
+
+    def outputs(self) -> dict:
+        return dict(dlogits=self.dlogits)
+
+
+def svd_logits_process_grad(dz, logits, stream=None, **kw) -> dict:
+    """One call; arguments as in :class:`LogitsProcessGrad`."""
+    return _once(LogitsProcessGrad, (dz, logits), kw, stream)
+
+
+class TreeVerify(_TreeOp):
+    """Greedy acceptance over a tree of drafts: ``node_tok`` [B, n] int32 with ``parent`` [B, n]
+    (default: a chain) and ``n_nodes`` [B], against the target's ``logits`` [B, n, V] bf16 or its
+    choice ``target_tok`` [B, n] int32 after every node.  Outputs: ``path`` [B, n] (nodes, -1
+    padded), ``n_path``, ``accept_len``, ``emitted`` [B, n], ``n_emitted`` and ``target_argmax``."""
+
+    _fn = "svd_tree_verify"
+
+    def __init__(self, node_tok, *, logits=None, target_tok=None, parent=None, n_nodes=None):
+        if (logits is None) == (target_tok is None):
+            raise ValueError("either logits or target_tok is required")
+        if node_tok.dim() != 2:
+            raise ValueError("node_tok is [B, n]")
+        B, n = node_tok.shape
+        dev, i32 = node_tok.device, torch.int32
+        a = TreeVerifyArgs()
+        if logits is not None:
+            if logits.dim() != 3:
+                raise ValueError("logits are [B, n, V]")
+            a.V = logits.shape[2]
+            a.T = _tensor(logits, "logits", torch.bfloat16, (B, n, a.V), dev)
+        a.target_tok = _tensor(target_tok, "target_tok", i32, (B, n), dev)
+        a.node_tok = _tensor(node_tok, "node_tok", i32, (B, n), dev)
+        a.parent = _tensor(parent, "parent", i32, (B, n), dev)
+        a.n_nodes = _tensor(n_nodes, "n_nodes", i32, (B,), dev)
+        a.B, a.n = B, n
+        new = lambda *shape: torch.empty(shape, dtype=i32, device=dev)  # noqa: E731
+        self.target_argmax, self.path, self.emitted = new(B, n), new(B, n), new(B, n)
+        self.n_path, self.accept_len, self.n_emitted = new(B), new(B), new(B)
+        for name in ("target_argmax", "path", "emitted", "n_path", "accept_len", "n_emitted"):
+            setattr(a, name, _ptr(getattr(self, name)))
+        self._set_up(a, lib().svd_tree_verify_workspace_bytes(B, n), dev,
+                     [logits, target_tok, node_tok, parent, n_nodes])
+
+    def outputs(self) -> dict:
+        return dict(target_argmax=self.target_argmax, path=self.path, n_path=self.n_path,
+                    accept_len=self.accept_len, emitted=self.emitted, n_emitted=self.n_emitted)
+
+
+def svd_tree_verify(node_tok, stream=None, **kw) -> dict:
+    """One call; arguments as in :class:`TreeVerify`."""
+    return _once(TreeVerify, (node_tok,), kw, stream)
+
+
+class CacheAppend(_TreeOp):
+    """Append of ``count`` [B] int32 entries of ``k_new``, ``v_new`` [B, n, Hkv, D] to the paged cache
+    behind ``cache_len`` [B]: the nodes ``path`` [B, n] names (``path`` and ``n_path`` of
+    :class:`TreeVerify`), or the first ones.  ``new_len`` may be ``cache_len`` (updated in place).
+    The cache is written in place.  Outputs: ``cache_k``, ``cache_v``, ``new_len`` [B]."""
+
+    _fn = "svd_cache_append"
+
+    def __init__(self, k_new, v_new, cache_k, cache_v, page_table, cache_len, count, *, path=None,
+                 new_len=None):
+        if k_new.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("expected bf16 or fp16 keys, got %s" % k_new.dtype)
+        if k_new.dim() != 4:
+            raise ValueError("k_new and v_new are [B, n, Hkv, D]")
+        B, n, Hkv, D = k_new.shape
+        dev, i32 = k_new.device, torch.int32
+        a = CacheAppendArgs()
+        a.k_new = _tensor(k_new, "k_new", k_new.dtype, (B, n, Hkv, D), dev)
+        a.v_new = _tensor(v_new, "v_new", k_new.dtype, (B, n, Hkv, D), dev)
+        a.cache_k, a.page_stride_k = _pages(cache_k, "cache_k", k_new.dtype, (Hkv, D), dev)
+        a.cache_v, a.page_stride_v = _pages(cache_v, "cache_v", k_new.dtype, (Hkv, D), dev)
+        if cache_k.shape != cache_v.shape:
+            raise ValueError("cache_k and cache_v differ in shape")
+        a.n_pages, a.page_size, a.max_pages = cache_k.shape[0], cache_k.shape[1], page_table.shape[-1]
+        a.page_table = _tensor(page_table, "page_table", i32, (B, a.max_pages), dev)
+        a.cache_len = _tensor(cache_len, "cache_len", i32, (B,), dev)
+        a.count = _tensor(count, "count", i32, (B,), dev)
+        a.path = _tensor(path, "path", i32, (B, n), dev)
+        a.B, a.n, a.Hkv, a.D = B, n, Hkv, D
+        self.cache_k, self.cache_v = cache_k, cache_v
+        self.new_len = torch.empty(B, dtype=i32, device=dev) if new_len is None else new_len
+        a.new_len = _tensor(self.new_len, "new_len", i32, (B,), dev)
+        self._set_up(a, lib().svd_cache_append_workspace_bytes(B), dev,
+                     [k_new, v_new, page_table, cache_len, count, path])
+
+    def outputs(self) -> dict:
+        return dict(cache_k=self.cache_k, cache_v=self.cache_v, new_len=self.new_len)
+
+
+def svd_cache_append(*args, stream=None, **kw) -> dict:
+    """One call; arguments as in :class:`CacheAppend`."""
+    return _once(CacheAppend, args, kw, stream)

@@ -337,6 +337,8 @@ const char* svd_status_string(svd_status s) {
         case SVD_ERR_TIMEOUT: return "SVD_ERR_TIMEOUT";
         case SVD_ERR_UNSUPPORTED: return "SVD_ERR_UNSUPPORTED";
         case SVD_ERR_TOKEN_RANGE: return "SVD_ERR_TOKEN_RANGE";
+        case SVD_ERR_PAGE_RANGE: return "SVD_ERR_PAGE_RANGE";
+        case SVD_ERR_TREE: return "SVD_ERR_TREE";
     }
     return "SVD_ERR_UNKNOWN";
 }
