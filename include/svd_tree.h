@@ -101,7 +101,7 @@ svd_status svd_tree_attention(const svd_tree_attention_args* args, void* ws, siz
  * The gradient with respect to the raw logits, with the counts and the mask of the same lists:
  *   dlogits = masked ? 0 : seen ? (x > 0 ? dz / repetition : dz * repetition) : dz
  * dlogits may be dz itself.
- * Limits: 1 <= n <= 64, 1 <= V <= 327680, hist_stride < 2^24, n_bias <= 4096, n_bias ids of one
+ * Limits: 1 <= n <= 64, 1 <= V <= 327680, hist_stride < 2^23, n_bias <= 4096, n_bias ids of one
  * sequence may repeat (their values add in list order).  V % 8 == 0 with 16-byte aligned logits,
  * out, dz and dlogits takes the fast path.
  * --------------------------------------------------------------------------------------------- */

@@ -1,14 +1,19 @@
 // logits_process.cu -- penalties, biases and grammar masks on the logits of a tree of drafts, and
 // the gradient of that map (include/svd_tree.h).
 //
-// Per element the map reads a logit and writes one, so it is bound by HBM: 4 bytes and an eighth
-// (the mask bit) per element, and nearly every element passes through unchanged or masked: only the
-// ids that the sequence has seen, or that carry a bias, need arithmetic.  A CTA owns a chunk of ids
-// of one sequence and all of its rows (or a group of them): it builds, once, a table of its chunk in
-// shared memory (one word per id: prompt flag, count in the generated history, index of the
-// drafted nodes with this token), and a bit per id that says whether the table has anything.  Each
-// thread keeps the bits of its own vectors in a register for all rows, so the common vector costs
-// a load, a mask byte and a store.
+// Per element the map reads a logit and writes one, so it is bound by HBM: 4 bytes and an eighth (the
+// mask bit) per element, and nearly every element passes through unchanged or masked: only the ids
+// that the sequence has seen, or that carry a bias, need arithmetic.  A CTA owns a chunk of ids of one
+// sequence and all of its rows (or a group of them).  Once, it builds a table of its chunk in shared
+// memory (one word per id: prompt flag, count in the generated history, index of the drafted nodes
+// with this token, bias) and the list of the ids that the table has anything for ("touched").  Rows then
+// stream through a two-stage ring of bulk copies, two rows a stage: all threads share the (row, touched
+// id) pairs of a stage and change those elements in shared memory, and behind one barrier every
+// thread takes whole vectors: mask, store, maximum.
+//
+// The pairs are what makes the touched ids cheap.  They are few and anywhere, so nearly every warp's
+// vectors hold one; worked on by the lane that holds its vector, they cost every warp the arithmetic
+// for one or two lanes (130 us at 32 x 17 rows of 151936 with 1536 tokens of history, 84 with the pairs).
 //
 // Ancestors' tokens differ from row to row.  They need no per-row table: the table names, for an
 // id that some node drafted, the set of nodes with that token (64 bits), and the row's count is
@@ -19,6 +24,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "tree_device.cuh"
 
@@ -28,72 +34,50 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr uint32_t kPrompt = 0x80000000u;   // table word: seen in the prompt
-constexpr int kSlotShift = 24;              // 7 bits: 1 + lowest node with this token
-constexpr uint32_t kCountMask = 0x00ffffffu;
+constexpr int kVecs = 2;                       // vectors of 8 ids per thread and row
+constexpr int kChunk = 8 * kVecs * kThreads;   // ids per CTA
+constexpr int kStages = 2;
+constexpr int kAhead = 4;                      // pairs per thread whose raw logits the gradient loads ahead
+constexpr int kStageBytes = 4 * kChunk;        // two rows of bf16 or one of fp32
+constexpr int kFewCtas = 444;                  // three per SM
+constexpr uint64_t kWaitNs = 1000000000ull;
 
-template <bool ALIGNED>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int v, int V) {
-    if (ALIGNED) return __ldcs(reinterpret_cast<const uint4*>(row + v));
-    uint32_t w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = v + e < V ? __ldg(row + v + e) : 0x7fffu;   // NaN: never an argmax
-    return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-}
-template <bool ALIGNED>
-__device__ __forceinline__ void store8(uint16_t* row, int v, int V, const uint4& x) {
-    if (ALIGNED) {
-        __stcs(reinterpret_cast<uint4*>(row + v), x);
-        return;
-    }
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (v + e < V) row[v + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
-}
-template <bool ALIGNED>
-__device__ __forceinline__ void load8(const float* row, int v, int V, float (&x)[8]) {
-    if (ALIGNED) {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(row + v));
-        const float4 b = __ldcs(reinterpret_cast<const float4*>(row + v) + 1);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = v + e < V ? row[v + e] : 0.f;
-}
-template <bool ALIGNED>
-__device__ __forceinline__ void store8(float* row, int v, int V, const float (&x)[8]) {
-    if (ALIGNED) {
-        __stcs(reinterpret_cast<float4*>(row + v), make_float4(x[0], x[1], x[2], x[3]));
-        __stcs(reinterpret_cast<float4*>(row + v) + 1, make_float4(x[4], x[5], x[6], x[7]));
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (v + e < V) row[v + e] = x[e];
-}
+// Table word of an id.
+constexpr uint32_t kPrompt = 0x80000000u;      // seen in the prompt
+constexpr int kSlotShift = 24;                 // 7 bits: 1 + lowest node with this token
+constexpr uint32_t kHasBias = 1u << 23;        // the rest of the word is the index of a bias entry, which
+                                               // holds the bias and the word
+constexpr uint32_t kCountMask = kHasBias - 1;  // count in the generated history
 
 struct Tables {
-    unsigned long long anc[kTreeMaxNodes];    // ancestors of every node
-    unsigned long long nodes[kTreeMaxNodes];  // nodes that share the token of their lowest one
-    unsigned long long key[kWarps][kTreeMaxNodes];
+    unsigned long long anc[kTreeMaxNodes];     // ancestors of every node
+    unsigned long long nodes[kTreeMaxNodes];   // nodes that share the token of their lowest one
+    uint4 best[kWarps][kTreeMaxNodes];         // each warp's best vector of each row,
+    int best_at[kWarps][kTreeMaxNodes];        // and its first id (-1: none)
+    uint64_t full[kStages];
+    int scan[kWarps];
     int tok[kTreeMaxNodes];
     int8_t parent[kTreeMaxNodes];
-    int last;
+    int last, repeated;
 };
 
+struct Dyn {                                   // dynamic shared memory
+    uint8_t* stage;                            // [kStages][kStageBytes]
+    uint32_t* tab;                             // [kChunk]
+    uint32_t* touched;                         // [kChunk / 32]
+    uint16_t* list;                            // [kChunk]: touched ids, ascending
+    uint32_t* bias_word;                       // [n_bias]
+    float* bias;                               // [n_bias]
+};
+constexpr size_t kDynBytes = kStages * kStageBytes + kChunk * 4 + kChunk / 8 + kChunk * 2;
+
 // Fills the chunk's table, touched bits and the ancestor sets; every thread of the CTA calls it.
-__device__ void build_tables(const LogitsParams& p, int b, int v0, int v1, bool grad, Tables& s,
-                             uint32_t* tab, float* bias, uint32_t* touched) {
+__device__ void build_tables(const LogitsParams& p, int b, int v0, int v1, int n_bias, Tables& s, const Dyn& d) {
     const svd_logits_process_args& a = p.a;
-    const int t = threadIdx.x, ch = p.chunk;
-    const bool has_bias = !grad && a.n_bias > 0;
-    for (int i = t; i < ch / 4; i += kThreads) reinterpret_cast<uint4*>(tab)[i] = make_uint4(0, 0, 0, 0);
-    if (has_bias)
-        for (int i = t; i < ch / 4; i += kThreads) reinterpret_cast<float4*>(bias)[i] = make_float4(0, 0, 0, 0);
-    for (int i = t; i < ch / 32; i += kThreads) touched[i] = 0;
+    const int t = threadIdx.x;
+    for (int i = t; i < kChunk / 4; i += kThreads) reinterpret_cast<uint4*>(d.tab)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = t; i < kChunk / 32; i += kThreads) d.touched[i] = 0;
+    if (t == 0) s.repeated = 0;
     if (t < kTreeMaxNodes) {
         s.nodes[t] = 0;
         s.tok[t] = -1;
@@ -106,7 +90,38 @@ __device__ void build_tables(const LogitsParams& p, int b, int v0, int v1, bool 
         }
     }
     __syncthreads();
-    auto touch = [&](int i) { atomicOr(&touched[i >> 5], 1u << (i & 31)); };
+    auto touch = [&](int i) { atomicOr(&d.touched[i >> 5], 1u << (i & 31)); };
+    const int32_t* bt = a.bias_tok + static_cast<size_t>(b) * a.n_bias;
+    const float* bv = a.bias_val + static_cast<size_t>(b) * a.n_bias;
+    if (n_bias > 0) {
+        for (int i = t; i < n_bias; i += kThreads) {
+            d.bias_word[i] = 0;
+            const int tok = __ldg(bt + i);
+            if (tok >= v0 && tok < v1) {
+                d.bias[i] = __ldg(bv + i);
+                if (atomicCAS(&d.tab[tok - v0], 0u, kHasBias | static_cast<uint32_t>(i)) != 0u) s.repeated = 1;
+                touch(tok - v0);
+            } else if (tok < -1 || tok >= a.V) {
+                set_device_error(p.status, SVD_ERR_TOKEN_RANGE);
+            }
+        }
+        __syncthreads();
+        if (s.repeated) {
+            // an id occurs more than once: its entry gets the sum of all of them, in list order
+            for (int i = t; i < n_bias; i += kThreads) {
+                const int tok = __ldg(bt + i);
+                if (tok < v0 || tok >= v1 || (d.tab[tok - v0] & kCountMask) != static_cast<uint32_t>(i)) continue;
+                float sum = 0.f;
+                for (int k = 0; k < n_bias; ++k)
+                    if (__ldg(bt + k) == tok) sum = __fadd_rn(sum, __ldg(bv + k));
+                d.bias[i] = sum;
+            }
+        }
+    }
+    auto word = [&](int at) {
+        const uint32_t w = n_bias > 0 ? d.tab[at] : 0u;
+        return w & kHasBias ? &d.bias_word[w & kCountMask] : &d.tab[at];
+    };
     if (a.history) {
         const int S = a.hist_stride;
         int hl = a.hist_len ? __ldg(a.hist_len + b) : S;
@@ -114,11 +129,12 @@ __device__ void build_tables(const LogitsParams& p, int b, int v0, int v1, bool 
         int pl = a.prompt_len ? __ldg(a.prompt_len + b) : 0;
         pl = pl < 0 ? 0 : (pl > hl ? hl : pl);
         const int32_t* h = a.history + static_cast<size_t>(b) * S;
+#pragma unroll 8
         for (int i = t; i < hl; i += kThreads) {
             const int tok = __ldg(h + i);
             if (tok >= v0 && tok < v1) {
-                if (i < pl) atomicOr(&tab[tok - v0], kPrompt);
-                else atomicAdd(&tab[tok - v0], 1u);
+                if (i < pl) atomicOr(word(tok - v0), kPrompt);
+                else atomicAdd(word(tok - v0), 1u);
                 touch(tok - v0);
             } else if (tok < -1 || tok >= a.V) {
                 set_device_error(p.status, SVD_ERR_TOKEN_RANGE);
@@ -133,29 +149,8 @@ __device__ void build_tables(const LogitsParams& p, int b, int v0, int v1, bool 
             while (s.tok[low] != tok) ++low;
             atomicOr(&s.nodes[low], 1ull << t);
             if (low == t) {
-                atomicOr(&tab[tok - v0], static_cast<uint32_t>(t + 1) << kSlotShift);
+                atomicOr(word(tok - v0), static_cast<uint32_t>(t + 1) << kSlotShift);
                 touch(tok - v0);
-            }
-        }
-    }
-    if (has_bias) {
-        const int32_t* bt = a.bias_tok + static_cast<size_t>(b) * a.n_bias;
-        const float* bv = a.bias_val + static_cast<size_t>(b) * a.n_bias;
-        for (int i = t; i < a.n_bias; i += kThreads) {
-            const int tok = __ldg(bt + i);
-            if (tok >= v0 && tok < v1) {
-                // the first entry of an id adds all of them, in list order
-                bool first = true;
-                for (int k = 0; k < i; ++k) first = first && __ldg(bt + k) != tok;
-                if (first) {
-                    float sum = __ldg(bv + i);
-                    for (int k = i + 1; k < a.n_bias; ++k)
-                        if (__ldg(bt + k) == tok) sum = __fadd_rn(sum, __ldg(bv + k));
-                    bias[tok - v0] = sum;
-                    touch(tok - v0);
-                }
-            } else if (tok < -1 || tok >= a.V) {
-                set_device_error(p.status, SVD_ERR_TOKEN_RANGE);
             }
         }
     }
@@ -170,138 +165,274 @@ __device__ __forceinline__ int row_count(uint32_t w, unsigned long long anc, con
     return c;
 }
 
-// GRAD: the gradient (dz -> dlogits), F32: dz and dlogits in fp32.  NV: vectors of 8 ids per thread.
-template <bool GRAD, bool F32, bool ALIGNED, int NV>
-__global__ void __launch_bounds__(kThreads) logits_process_kernel(LogitsParams p) {
-    extern __shared__ __align__(16) uint32_t dyn[];
+// prmt with the selector's replicate-sign bits (__byte_perm takes three bits of each selector only).
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(a), "r"(sel));
+    return r;
+}
+// Elements whose bit in `m` is clear become `fill` (two copies of 16 bits): each bit is spread to the
+// sign of a byte, and the byte permutation replicates signs over 16 bits.
+__device__ __forceinline__ uint4 mask16(const uint4& x, uint32_t m, uint32_t fill) {
+    const uint32_t lo = ((m & 15u) * 0x00204081u & 0x01010101u) << 7, hi = ((m >> 4 & 15u) * 0x00204081u & 0x01010101u) << 7;
+    const uint32_t k0 = prmt(lo, 0x9988), k1 = prmt(lo, 0xbbaa);
+    const uint32_t k2 = prmt(hi, 0x9988), k3 = prmt(hi, 0xbbaa);
+    return make_uint4((x.x & k0) | (fill & ~k0), (x.y & k1) | (fill & ~k1), (x.z & k2) | (fill & ~k2), (x.w & k3) | (fill & ~k3));
+}
+// Writes the first `left` (at most 8) elements of a vector where the rows are not aligned.
+template <class T>
+__device__ __forceinline__ void store_some(T* to, const T (&x)[8], int left) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < left) to[e] = x[e];
+}
+
+// GRAD: the gradient (dz -> dlogits), F32: dz and dlogits in fp32.
+template <bool GRAD, bool F32, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, 3) logits_process_kernel(LogitsParams p) {
+    using T = typename std::conditional<F32, float, uint16_t>::type;
+    constexpr int kRows = F32 ? 1 : 2;                    // rows per stage
+    extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ Tables s;
     const svd_logits_process_args& a = p.a;
-    const int t = threadIdx.x, lane = t & 31, b = blockIdx.y, V = a.V;
-    const int v0 = blockIdx.x * p.chunk, v1 = min(V, v0 + p.chunk);
+    const int t = threadIdx.x, lane = t & 31, b = blockIdx.x, V = a.V;
+    const int v0 = blockIdx.y * kChunk, v1 = min(V, v0 + kChunk);
     const int j0 = blockIdx.z * p.rows_per_cta, j1 = min(a.n, j0 + p.rows_per_cta);
-    uint32_t* tab = dyn;
-    uint32_t* touched = dyn + p.chunk;
-    float* bias = reinterpret_cast<float*>(touched + p.chunk / 32);
-    const bool has_bias = !GRAD && a.n_bias > 0;
-    build_tables(p, b, v0, v1, GRAD, s, tab, bias, touched);
+    const int n_bias = GRAD ? 0 : a.n_bias;
+    Dyn d;
+    d.stage = dyn;
+    d.tab = reinterpret_cast<uint32_t*>(dyn + kStages * kStageBytes);
+    d.touched = d.tab + kChunk;
+    d.list = reinterpret_cast<uint16_t*>(d.touched + kChunk / 32);
+    d.bias_word = reinterpret_cast<uint32_t*>(d.list + kChunk);
+    d.bias = reinterpret_cast<float*>(d.bias_word + n_bias);
+
+    const bool want_arg = !GRAD && a.argmax != nullptr;
+    const size_t row0 = static_cast<size_t>(b) * a.n;
+    const uint16_t* const raw = a.logits + row0 * V;
+    const T* const src = GRAD ? static_cast<const T*>(a.dz) + row0 * V : reinterpret_cast<const T*>(raw);
+    T* const dst = GRAD ? static_cast<T*>(a.dlogits) + row0 * V
+                        : (a.out ? reinterpret_cast<T*>(a.out) + row0 * V : nullptr);
+    // in place without a mask only the touched elements are read and written
+    const bool sparse = src == dst && !want_arg && !a.mask;
+    const int batches = sparse ? 0 : (j1 - j0 + kRows - 1) / kRows;
+
+    // rows of batch k into its stage
+    auto fetch = [&](int k) {
+        uint8_t* to = d.stage + (k % kStages) * kStageBytes;
+        const int j = j0 + k * kRows, rows = min(kRows, j1 - j);
+        if (ALIGNED) {
+            if (t != 0) return;
+            const uint32_t bytes = static_cast<uint32_t>(v1 - v0) * sizeof(T);
+            mbar_arrive_expect_tx(&s.full[k % kStages], rows * bytes);
+            for (int r = 0; r < rows; ++r)
+                bulk_load(to + r * kChunk * sizeof(T), src + static_cast<size_t>(j + r) * V + v0, bytes, &s.full[k % kStages]);
+        } else {
+            for (int r = 0; r < rows; ++r)
+                for (int i = t; i < v1 - v0; i += kThreads)
+                    reinterpret_cast<T*>(to)[r * kChunk + i] = src[static_cast<size_t>(j + r) * V + v0 + i];
+        }
+    };
+    if (ALIGNED && t == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1);
+        fence_mbar_init();
+    }
+    // the first rows arrive while the table is built
+    for (int k = 0; k < kStages && k < batches; ++k) fetch(k);
+    build_tables(p, b, v0, v1, n_bias, s, d);
+
+    // the list of touched ids
+    const uint32_t tw = t < kChunk / 32 ? d.touched[t] : 0u;
+    int n_touched;
+    {
+        const int mine = __popc(tw);
+        int rank = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, rank, o);
+            if (lane >= o) rank += y;
+        }
+        if (lane == 31) s.scan[t >> 5] = rank;
+        __syncthreads();
+        n_touched = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < (t >> 5)) rank += s.scan[w];
+            n_touched += s.scan[w];
+        }
+        rank -= mine;
+        for (uint32_t bits = tw; bits; bits &= bits - 1) d.list[rank++] = static_cast<uint16_t>(t * 32 + __ffs(bits) - 1);
+    }
+    __syncthreads();
 
     const float rep = a.repetition ? __ldg(a.repetition + b) : 1.f;
     const float freq = !GRAD && a.frequency ? __ldg(a.frequency + b) : 0.f;
     const float pres = !GRAD && a.presence ? __ldg(a.presence + b) : 0.f;
-    const bool want_arg = !GRAD && a.argmax != nullptr;
-    // in place, a vector that nothing changes needs neither its load nor its store
-    const bool in_place = GRAD ? a.dz == a.dlogits : a.logits == a.out;
-    const bool may_skip = in_place && !want_arg;
-    const size_t W = static_cast<size_t>((V + 31) / 32);
+    auto f32 = [](uint16_t w) { return __uint_as_float(static_cast<uint32_t>(w) << 16); };
+    // the new value of id v0 + at in row j: x is the raw logit, or dz with the sign of the raw logit
+    auto changed = [&](float x, bool positive, int at, int j) {
+        uint32_t w = d.tab[at], entry = 0;
+        const bool has_bias = n_bias > 0 && (w & kHasBias);
+        if (has_bias) {
+            entry = w & kCountMask;
+            w = d.bias_word[entry];
+        }
+        const int c = row_count(w, a.node_tok ? s.anc[j] : 0ull, s);
+        if (c > 0 || (w & kPrompt)) x = positive ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
+        if (!GRAD) {
+            x = __fsub_rn(x, __fmul_rn(freq, static_cast<float>(c)));
+            if (c > 0) x = __fsub_rn(x, pres);
+            if (has_bias) x = __fadd_rn(x, d.bias[entry]);
+        }
+        return x;
+    };
+    auto as_f32 = [&](T x) { return F32 ? static_cast<float>(x) : f32(static_cast<uint16_t>(x)); };
+    auto as_t = [&](float x) { return F32 ? static_cast<T>(x) : static_cast<T>(__bfloat16_as_ushort(__float2bfloat16_rn(x))); };
 
-    int vv[NV];
-    uint32_t tb[NV], mb1[NV];
-    const uint8_t* mask = reinterpret_cast<const uint8_t*>(a.mask);
-#pragma unroll
-    for (int q = 0; q < NV; ++q) {
-        vv[q] = v0 + (q * kThreads + t) * 8;
-        tb[q] = vv[q] < v1 ? reinterpret_cast<const uint8_t*>(touched)[(vv[q] - v0) >> 3] : 0u;
-        mb1[q] = 0xffu;
-        if (mask && a.mask_rows == 1 && vv[q] < v1) mb1[q] = __ldg(mask + b * W * 4 + (vv[q] >> 3));
+    if (sparse) {
+        for (int i = t; i < n_touched * (j1 - j0); i += kThreads) {
+            const int at = d.list[i % n_touched], j = j0 + i / n_touched;
+            const size_t e = static_cast<size_t>(j) * V + v0 + at;
+            const float x = as_f32(dst[e]);
+            dst[e] = as_t(changed(x, GRAD ? f32(__ldg(raw + e)) > 0.f : x > 0.f, at, j));
+        }
+        return;
     }
-    const uint16_t mval = __bfloat16_as_ushort(__float2bfloat16_rn(GRAD ? 0.f : a.mask_value));
 
-    for (int j = j0; j < j1; ++j) {
-        const size_t row = static_cast<size_t>(b) * a.n + j;
-        const size_t off = row * V;
-        const unsigned long long anc = a.node_tok ? s.anc[j] : 0ull;
-        uint4 best = make_uint4(0, 0, 0, 0);
-        float best_m = -INFINITY;
-        int best_at = -1;
-        uint4 xs[NV];
-        uint32_t ms[NV];
+    const size_t W4 = static_cast<size_t>((V + 31) / 32) * 4;
+    const bool row_mask = a.mask && a.mask_rows != 1;
+    const uint8_t* const mask = reinterpret_cast<const uint8_t*>(a.mask) + (row_mask ? row0 : static_cast<size_t>(b)) * W4;
+    const uint32_t mval = __bfloat16_as_ushort(__float2bfloat16_rn(GRAD ? 0.f : a.mask_value));
+    const uint32_t fill = mval | mval << 16;
+    const int pairs = n_touched * kRows;
+    // mask bytes of a batch, and the gradient's raw logits of this thread's first pairs, go out a batch ahead
+    uint32_t ms[kRows][kVecs];
+    uint16_t raws[kAhead] = {};
+    auto prefetch = [&](int k) {
 #pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            ms[q] = mb1[q];
-            if (mask && a.mask_rows != 1 && vv[q] < v1) ms[q] = __ldg(mask + row * W * 4 + (vv[q] >> 3));
-            if (!F32 && vv[q] < v1 && !(may_skip && tb[q] == 0u && ms[q] == 0xffu))
-                xs[q] = load8<ALIGNED>((GRAD ? static_cast<const uint16_t*>(a.dz) : a.logits) + off, vv[q], V);
+        for (int r = 0; r < kRows; ++r) {
+            const int j = j0 + k * kRows + r;
+#pragma unroll
+            for (int q = 0; q < kVecs; ++q) {
+                const int v = v0 + (q * kThreads + t) * 8;
+                if (a.mask && j < j1 && v < v1) ms[r][q] = __ldg(mask + (row_mask ? j * W4 : 0) + (v >> 3));
+            }
         }
 #pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            const int v = vv[q];
-            if (v >= v1 || (may_skip && tb[q] == 0u && ms[q] == 0xffu)) continue;
-            if (F32) {
-                float d[8];
-                load8<ALIGNED>(static_cast<const float*>(a.dz) + off, v, V, d);
-                if (tb[q]) {
-                    float x[8];
-                    unpack8(load8<ALIGNED>(a.logits + off, v, V), x);
+        for (int u = 0; GRAD && u < kAhead; ++u) {
+            const int i = t + u * kThreads, j = j0 + k * kRows + i % kRows;
+            if (i < pairs && j < j1) raws[u] = __ldg(raw + static_cast<size_t>(j) * V + v0 + d.list[i / kRows]);
+        }
+    };
+    prefetch(0);
+
+    bool ok = true;
+    for (int k = 0; k < batches; ++k) {
+        T* const st = reinterpret_cast<T*>(d.stage + (k % kStages) * kStageBytes);
+        const int jb = j0 + k * kRows;
+        if (ALIGNED) ok = mbar_wait_bounded(&s.full[k % kStages], (k / kStages) & 1, kWaitNs);
+        else __syncthreads();   // the stage was filled by all threads
+        auto pair = [&](int i, uint16_t raw_logit) {
+            const int r = i % kRows, at = d.list[i / kRows];
+            const float x = as_f32(st[r * kChunk + at]);
+            st[r * kChunk + at] = as_t(changed(x, GRAD ? f32(raw_logit) > 0.f : x > 0.f, at, jb + r));
+        };
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t w = (tb[q] >> e & 1u) ? tab[v - v0 + e] : 0u;
-                        if (w && ((w & kPrompt) || row_count(w, anc, s) > 0))
-                            d[e] = x[e] > 0.f ? __fdiv_rn(d[e], rep) : __fmul_rn(d[e], rep);
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = t + u * kThreads;
+            if (i < pairs && jb + i % kRows < j1) pair(i, raws[u]);
+        }
+        for (int i = t + kAhead * kThreads; i < pairs; i += kThreads)
+            if (jb + i % kRows < j1)
+                pair(i, GRAD ? __ldg(raw + static_cast<size_t>(jb + i % kRows) * V + v0 + d.list[i / kRows]) : uint16_t(0));
+        // One barrier a batch: the pairs are done, and every thread has left the batch before, whose
+        // stage is filled anew.
+        if (ALIGNED) fence_async();
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        if (k > 0 && k - 1 + kStages < batches) fetch(k - 1 + kStages);
+        uint32_t mk[kRows][kVecs];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int q = 0; q < kVecs; ++q) mk[r][q] = a.mask ? ms[r][q] : 0xffu;
+        if (k + 1 < batches) prefetch(k + 1);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int j = jb + r;
+            if (j >= j1) break;
+            float best_m = __int_as_float(0x7fffffff);   // NaN: no vector yet
+            uint4 best = make_uint4(0, 0, 0, 0);
+            int best_at = -1;
+#pragma unroll
+            for (int q = 0; q < kVecs; ++q) {
+                const int i8 = (q * kThreads + t) * 8, v = v0 + i8;
+                if (v >= v1) continue;
+                const size_t off = static_cast<size_t>(j) * V + v;
+                if (F32) {
+                    const float4 lo = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(st) + i8);
+                    const float4 hi = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(st) + i8 + 4);
+                    float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = mk[r][q] >> e & 1u ? x[e] : 0.f;
+                    float* to = reinterpret_cast<float*>(dst) + off;
+                    if (ALIGNED) {
+                        __stcs(reinterpret_cast<float4*>(to), make_float4(x[0], x[1], x[2], x[3]));
+                        __stcs(reinterpret_cast<float4*>(to) + 1, make_float4(x[4], x[5], x[6], x[7]));
+                    } else {
+                        store_some(to, x, V - v);
+                    }
+                    continue;
+                }
+                uint4 x = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(st) + r * kChunk + i8);
+                if (a.mask) x = mask16(x, mk[r][q], fill);
+                if (dst) {
+                    uint16_t* to = reinterpret_cast<uint16_t*>(dst) + off;
+                    if (ALIGNED) {
+                        __stcs(reinterpret_cast<uint4*>(to), x);
+                    } else {
+                        const uint16_t w[8] = {static_cast<uint16_t>(x.x), static_cast<uint16_t>(x.x >> 16),
+                                               static_cast<uint16_t>(x.y), static_cast<uint16_t>(x.y >> 16),
+                                               static_cast<uint16_t>(x.z), static_cast<uint16_t>(x.z >> 16),
+                                               static_cast<uint16_t>(x.w), static_cast<uint16_t>(x.w >> 16)};
+                        store_some(to, w, V - v);
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (!(ms[q] >> e & 1u)) d[e] = 0.f;
-                store8<ALIGNED>(static_cast<float*>(a.dlogits) + off, v, V, d);
-                continue;
-            }
-            uint4 x4 = xs[q];
-            if (tb[q]) {
-                float x[8], r[8];
-                unpack8(x4, x);
-                if (GRAD) unpack8(load8<ALIGNED>(a.logits + off, v, V), r);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (!(tb[q] >> e & 1u)) continue;
-                    const uint32_t w = tab[v - v0 + e];
-                    const int c = row_count(w, anc, s);
-                    if (c > 0 || (w & kPrompt)) {
-                        const bool pos = GRAD ? r[e] > 0.f : x[e] > 0.f;
-                        x[e] = pos ? __fdiv_rn(x[e], rep) : __fmul_rn(x[e], rep);
-                    }
-                    if (!GRAD) {
-                        x[e] = __fsub_rn(x[e], __fmul_rn(freq, static_cast<float>(c)));
-                        if (c > 0) x[e] = __fsub_rn(x[e], pres);
-                        if (has_bias) x[e] = __fadd_rn(x[e], bias[v - v0 + e]);
-                    }
-                }
-                x4 = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                pack_bf16x2(x[6], x[7]));
-            }
-            if (ms[q] != 0xffu) {
-                uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t keep = 0xffffu << (16 * (e & 1));
-                    if (!(ms[q] >> e & 1u)) w[e >> 1] = (w[e >> 1] & ~keep) | (static_cast<uint32_t>(mval) << (16 * (e & 1)));
-                }
-                x4 = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            if (GRAD) {
-                store8<ALIGNED>(static_cast<uint16_t*>(a.dlogits) + off, v, V, x4);
-            } else {
-                if (a.out) store8<ALIGNED>(a.out + off, v, V, x4);
                 if (want_arg) {
-                    if (!ALIGNED && v + 8 > V) {   // the mask wrote over the padding behind V
-                        uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
+                    if (!ALIGNED && v + 8 > V) {   // what lies behind V becomes NaN: no candidate
+                        uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             if (v + e >= V) w[e >> 1] |= 0x7fffu << (16 * (e & 1));
-                        x4 = make_uint4(w[0], w[1], w[2], w[3]);
+                        x = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    const float m = max8_bf16(x4);
-                    if (best_at < 0 || m > best_m || (best_m != best_m && m == m)) {
-                        best = x4;
+                    const float m = max8_bf16(x);
+                    if (m > best_m || best_m != best_m) {
+                        best = x;
                         best_m = m;
                         best_at = v;
                     }
                 }
             }
+            if (want_arg) {
+                // the warp's best vector; of equal ones the lowest ids: first by q, then by lane
+                const bool num = best_m == best_m;
+                const float top = redux_max_f32(num ? best_m : -INFINITY);
+                const unsigned win = __ballot_sync(0xffffffffu, num && best_m == top);
+                const unsigned low = __ballot_sync(0xffffffffu, num && best_m == top && best_at == v0 + t * 8);
+                if (lane == (win ? __ffs(low ? low : win) - 1 : 0)) {
+                    s.best[t >> 5][j - j0] = best;
+                    s.best_at[t >> 5][j - j0] = win ? best_at : -1;
+                }
+            }
         }
-        if (want_arg) {
-            const unsigned long long key = warp_best_key(best_at >= 0, best, best_at);
-            if (lane == 0) s.key[t >> 5][j - j0] = key;
+    }
+    if (!ok) {   // a copy did not arrive in time: record it, and leave no copy in flight
+        if (t == 0) {
+            set_device_error(p.status, SVD_ERR_TIMEOUT);
+            for (int i = 0; i < kStages; ++i) mbar_wait_bounded(&s.full[i], 0, kWaitNs), mbar_wait_bounded(&s.full[i], 1, kWaitNs);
         }
+        return;
     }
     if (!want_arg) return;
     // one atomic maximum per row and CTA (a maximum does not depend on the order); the last CTA of
@@ -309,48 +440,59 @@ __global__ void __launch_bounds__(kThreads) logits_process_kernel(LogitsParams p
     __syncthreads();
     if (t < j1 - j0) {
         unsigned long long key = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) key = max(key, s.key[w][t]);
-        if (key) atomicMax(&p.key[static_cast<size_t>(b) * a.n + j0 + t], key);
+        for (int w = 0; w < kWarps; ++w) {
+            if (s.best_at[w][t] < 0) continue;
+            const uint4 x = s.best[w][t];
+            const float m = max8_bf16(x);
+            key = max(key, argmax_key(m, s.best_at[w][t] + first_pos(x, m)));
+        }
+        if (key) atomicMax(&p.key[row0 + j0 + t], key);
         __threadfence();
     }
     __syncthreads();
-    if (t == 0) s.last = atomicAdd(&p.ticket[b], 1u) == gridDim.x * gridDim.z - 1;
+    if (t == 0) s.last = atomicAdd(&p.ticket[b], 1u) == gridDim.y * gridDim.z - 1;
     __syncthreads();
     if (!s.last) return;
     __threadfence();
     if (t < a.n) {
-        const size_t row = static_cast<size_t>(b) * a.n + t;
-        a.argmax[row] = argmax_id(__ldcg(&p.key[row]));
-        p.key[row] = 0ull;
+        a.argmax[row0 + t] = argmax_id(__ldcg(&p.key[row0 + t]));
+        p.key[row0 + t] = 0ull;
     }
     if (t == 0) p.ticket[b] = 0u;
 }
 
-template <bool GRAD, bool F32, bool ALIGNED, int NV>
-cudaError_t launch(const LogitsParams& p, dim3 grid, cudaStream_t st) {
-    const size_t words = static_cast<size_t>(p.chunk) + p.chunk / 32 + (!GRAD && p.a.n_bias > 0 ? p.chunk : 0);
-    logits_process_kernel<GRAD, F32, ALIGNED, NV><<<grid, kThreads, words * 4, st>>>(p);
+template <bool GRAD, bool F32, bool ALIGNED>
+cudaError_t launch(const LogitsParams& in, cudaStream_t st) {
+    LogitsParams p = in;
+    const int chunks = (p.a.V + kChunk - 1) / kChunk;
+    // rows are split over CTAs only where the chunks alone leave SMs without work: every split builds
+    // the chunk's table again
+    int splits = kFewCtas / (chunks * p.a.B);
+    splits = splits < 1 ? 1 : (splits > p.a.n ? p.a.n : splits);
+    p.rows_per_cta = (p.a.n + splits - 1) / splits;
+    // low ids, which have the most touched ones, start first and do not end up in the tail
+    const dim3 grid(p.a.B, chunks, (p.a.n + p.rows_per_cta - 1) / p.rows_per_cta);
+    const size_t bytes = kDynBytes + (GRAD ? 0 : 8 * static_cast<size_t>(p.a.n_bias));
+    const cudaError_t e = cudaFuncSetAttribute(logits_process_kernel<GRAD, F32, ALIGNED>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kDynBytes + 8 * 4096));
+    if (e != cudaSuccess) return e;
+    logits_process_kernel<GRAD, F32, ALIGNED><<<grid, kThreads, bytes, st>>>(p);
     return cudaGetLastError();
 }
 
-template <bool GRAD, bool F32, int NV>
-cudaError_t launch_al(const LogitsParams& p, dim3 grid, cudaStream_t st) {
-    return p.aligned ? launch<GRAD, F32, true, NV>(p, grid, st) : launch<GRAD, F32, false, NV>(p, grid, st);
+template <bool GRAD, bool F32>
+cudaError_t launch_al(const LogitsParams& p, cudaStream_t st) {
+    return p.aligned ? launch<GRAD, F32, true>(p, st) : launch<GRAD, F32, false>(p, st);
 }
 
 }  // namespace
 
-int launch_logits_process(const LogitsParams& in, bool grad, void* stream) {
-    LogitsParams p = in;
+int launch_logits_process(const LogitsParams& p, bool grad, void* stream) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    p.chunk = 8 * kThreads;
-    p.rows_per_cta = p.a.n;
-    const dim3 grid((p.a.V + p.chunk - 1) / p.chunk, p.a.B, (p.a.n + p.rows_per_cta - 1) / p.rows_per_cta);
     cudaError_t e;
-    if (!grad) e = launch_al<false, false, 1>(p, grid, st);
-    else if (p.a.grad_fp32) e = launch_al<true, true, 1>(p, grid, st);
-    else e = launch_al<true, false, 1>(p, grid, st);
+    if (!grad) e = launch_al<false, false>(p, st);
+    else if (p.a.grad_fp32) e = launch_al<true, true>(p, st);
+    else e = launch_al<true, false>(p, st);
     return static_cast<int>(e);
 }
 

@@ -11,11 +11,6 @@ namespace svd {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-// Generic-proxy writes to shared memory before this are visible to the async proxy (TMA, tcgen05) after it.
-__device__ __forceinline__ void fence_async_smem() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 // Box of a 4-dimensional tensor map to this CTA's shared memory (no multicast); c0 * element size is
 // a multiple of 16 bytes.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,

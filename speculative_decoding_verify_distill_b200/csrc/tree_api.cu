@@ -13,7 +13,7 @@ namespace {
 
 constexpr int kMaxV = 327680;
 constexpr int kMaxBias = 4096;
-constexpr int kMaxHistory = 1 << 24;   // counts are kept in 24 bits
+constexpr int kMaxHistory = 1 << 23;   // counts are kept in 23 bits
 constexpr int kMaxGridYZ = 65535;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

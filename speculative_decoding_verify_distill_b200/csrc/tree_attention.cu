@@ -385,14 +385,14 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                             mbar_arrive(&ctl.aux);
                         }
                         ++naux;
-                        fence_async_smem();
+                        fence_async();
                         __syncwarp();
                     } else if (valid < steps * 16) {
                         for (int i = lane; i < (steps * 16 - valid) * kHalves * 8; i += 32) {
                             const int row = valid + i / (kHalves * 8), ch = i % (kHalves * 8);
                             *reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + row * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
                         }
-                        fence_async_smem();
+                        fence_async();
                         __syncwarp();
                     }
                 }
@@ -447,7 +447,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                     x[ch].x ^= flip; x[ch].y ^= flip; x[ch].z ^= flip; x[ch].w ^= flip;
                     *reinterpret_cast<uint4*>(dst + (ch >> 3) * kHalfBytes + (((ch & 7) ^ (trow & 7)) << 4)) = x[ch];
                 }
-                fence_async_smem();
+                fence_async();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.q_full[rt]);

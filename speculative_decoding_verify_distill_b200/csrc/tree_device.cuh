@@ -24,6 +24,11 @@ __device__ __forceinline__ int checked_parent(const int32_t* parent, size_t row,
     return -1;
 }
 
+// Generic-proxy accesses to shared memory before this are ordered before the async proxy's after it.
+__device__ __forceinline__ void fence_async() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // A key that orders bf16 values (no NaN; -0 is taken as +0) and, among equal ones, lower ids first.
 __device__ __forceinline__ unsigned long long argmax_key(float v, int id) {
     const uint32_t b = __float_as_uint(v + 0.0f);

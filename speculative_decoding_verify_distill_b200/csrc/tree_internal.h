@@ -27,7 +27,6 @@ __host__ __device__ inline LogitsWs logits_ws(int B, int n) {
 struct LogitsParams {
     svd_logits_process_args a;
     int aligned;       // 16-byte vectors; 0: element loads and stores
-    int chunk;         // ids per CTA, a multiple of 8 * kLogitsThreads
     int rows_per_cta;
     uint32_t* status;
     unsigned long long* key;   // [B, n]
@@ -38,7 +37,6 @@ int launch_logits_process(const LogitsParams& p, bool grad, void* stream);
 struct VerifyParams {
     svd_tree_verify_args a;
     int aligned;
-    int chunk;         // ids per CTA
     uint32_t* status;
     unsigned long long* key;
     uint32_t* ticket;
