@@ -4,25 +4,28 @@
 // What bounds it: every cached key and value is read once (2 x 2 bytes x D per key head and token)
 // and serves the n * Hq / Hkv query rows of its head.  Up to about 128 rows that is less than the
 // tensor cores' rate over HBM's, so the kernel streams the cache through shared memory and does all
-// arithmetic behind it.
+// arithmetic behind it; with more rows the softmax bounds it (16 exponentials a clock and SM).
 //
-// Work.  An item is one sequence, key head and group of up to R * 128 query rows (a row is a node
-// and a query head; R = 1 or 2 row tiles); its keys are tiles of 128: the cached ones, then one tile of
-// the drafted nodes.  All tiles of all items form one line that is cut into equal parts, one per CTA
-// (148, one per SM), so ragged lengths balance by themselves and one long sequence spreads over the
-// whole GPU.  A part that holds a whole item writes its result; otherwise it leaves the unnormalised
-// sum with the row maxima and sums in the workspace, and a second kernel (a programmatic dependent,
-// its launch hidden) joins the parts in a fixed order.
+// Work.  An item is one sequence and key head; its keys are tiles of 128: the cached ones, then one tile of
+// the drafted nodes.  All tiles of all items form one line that is cut into equal parts, so ragged
+// lengths balance by themselves and one long sequence spreads over the whole GPU.  A CTA takes one part for
+// one group of 128 query rows (a row is a node and a query head); the CTAs of the same part and different
+// groups run side by side and share the part's keys through L2.  A part that holds a whole item writes its
+// result; otherwise it leaves the unnormalised sum with the row maxima and sums in the workspace, and a
+// second kernel (a programmatic dependent, its launch hidden) joins the parts in a fixed order.
 //
 // Roles in a CTA.  A producer warp loads K and V tiles page by page by TMA (128-byte swizzle) into a
-// ring; one warp issues tcgen05.mma: S = Q K^T into TMEM, O += P V with P read from TMEM; one
-// softmax warpgroup per row tile: thread = row, so maxima and sums need no exchange.  It reads S,
-// keeps a running maximum that moves only when a tile exceeds it by more than 2^8 (the sum and O
-// share the stale reference, so the quotient is exact all the same, and O in TMEM is rescaled
-// rarely), and writes P = exp2(S - m) over S in the tensors' type (that rounding, at most half a step of
-// the type per weight, is what the matrix instruction takes; maxima and sums stay fp32).  With one row
-// tile S is double buffered, so the next tile's S forms while this tile's softmax runs; with two,
-// the row tiles alternate.
+// ring; one warp issues tcgen05.mma: S = Q K^T into one of three TMEM slots, up to two tiles ahead, and
+// O += P V with P read from TMEM; two softmax warpgroups take the tiles in turn, thread = row, so the
+// sums and maxima of a tile need no exchange.  A warpgroup reads S and moves the row's reference maximum
+// only when a tile exceeds it by more than 2^8 (the sums and O share the stale reference, so the quotient
+// is exact all the same, and O in TMEM is rescaled rarely), hands the reference to the other warpgroup, and
+// writes P = exp2(S - m) over S in the tensors' type (that rounding, at most half a step of the type
+// per weight, is what the matrix instruction takes; maxima and sums stay fp32).  A warp needs about 2200
+// cycles for a tile, of which 1024 are its exponentials, and a tile's bytes take 2800 at HBM's rate: one
+// warpgroup alone was too slow beside the waits, and so were two that split the columns.  Where an item
+// ends, Q of the next one is fetched behind the last tile's softmax, and its first S forms while O is
+// written out.
 //
 // Masks.  Columns behind the cache length and nodes that are not ancestors get P = 0 whatever S
 // holds.  0 * NaN would still reach O through the matrix product, so rows of V behind the length
@@ -41,41 +44,46 @@ namespace svd {
 
 namespace {
 
-constexpr int kCtas = 148;         // parts of the line of tiles: one per SM of a B200
-constexpr int kTile = 128;         // keys per tile, rows per row tile
+constexpr int kCtas = 148;         // one per SM of a B200
+constexpr int kTile = 128;         // keys per tile, rows per group
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kCombineWarps = 8;
+constexpr int kLens = 64;          // sequences of a part whose lengths are kept in shared memory
 
 struct PartInfo {                  // what the combine kernel needs to know of the item that starts in a
-    int b, hk, rg, last;           // part and does not end there: last part it reaches, or -1
+    int b, hk, last;               // part and does not end there: last part it reaches, or -1
 };
 
 struct AttnWs {
     size_t info, ml, o, total;
 };
-__host__ __device__ inline int row_tiles(int rows) { return rows > kTile ? 2 : 1; }
+// Row groups, the parts that the line is cut into at most, and CTAs (more than one per SM only where a
+// key head has more than 148 row groups).
+__host__ __device__ inline int row_groups(int rows) { return (rows + kTile - 1) / kTile; }
+__host__ __device__ inline int max_parts(int groups) { return groups >= kCtas ? 1 : kCtas / groups; }
 inline AttnWs attn_ws(int rows, int D) {
-    const int used = rows < row_tiles(rows) * kTile ? rows : row_tiles(rows) * kTile;
+    const size_t used = rows < kTile ? rows : kTile, groups = row_groups(rows);
+    const size_t ctas = groups * max_parts(static_cast<int>(groups));
     AttnWs L;
     L.info = sizeof(WsHeader);
-    L.ml = align256(L.info + sizeof(PartInfo) * kCtas);
-    L.o = align256(L.ml + sizeof(float2) * 2 * kCtas * static_cast<size_t>(used));
-    L.total = align256(L.o + sizeof(float) * 2 * kCtas * static_cast<size_t>(used) * static_cast<size_t>(D));
+    L.ml = align256(L.info + sizeof(PartInfo) * ctas);
+    L.o = align256(L.ml + sizeof(float2) * 2 * ctas * used);
+    L.total = align256(L.o + sizeof(float) * 2 * ctas * used * static_cast<size_t>(D));
     return L;
 }
 
 struct alignas(64) AttnParams {
     CUtensorMap ck, cv, nk, nv;    // cache and drafted nodes
     svd_tree_attention_args a;
-    int G, rows, used, NR;         // heads per key head, rows per item line, rows kept per slot, row groups
+    int G, rows, used, NR;         // heads per key head, its query rows, rows kept per slot, row groups
     int page_rows, page_shift;     // rows per TMA box, log2(page_size)
     int nb;                        // columns of the drafted tile, a multiple of 16
     float c, thr;                  // |scale| log2(e); 8 / c
     int qflip, qzero;              // the sign of the scale goes to Q; a scale of 0 zeroes Q
     uint32_t* status;
-    PartInfo* info;
-    float2* ml;                    // [2 kCtas][used]: running maximum (raw scores), sum
-    float* o;                      // [2 kCtas][used][D]
+    PartInfo* info;                // [CTAs]
+    float2* ml;                    // [2 CTAs][used]: reference maximum (raw scores), sum
+    float* o;                      // [2 CTAs][used][D]
 };
 
 // Tiles of sequence b: its cached ones and the drafted one.
@@ -88,28 +96,38 @@ __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kT
 
 // A run of tiles of one item within this CTA's part.
 struct Segment {
-    int b, hk, rg, len;
+    int b, hk, len;
     int tile0, tile1, tiles;
 };
+// Steps through the segments of the part [lo, hi) of the line of tiles; `base` is where sequence b begins.
 struct Walker {
-    long long pos, hi, base;
-    int b;
-    __device__ bool next(const AttnParams& p, Segment& s) {
-        if (pos >= hi) return false;
-        while (true) {
-            s.len = cache_len_of(p, b);
-            s.tiles = tiles_of(s.len);
-            const long long w = static_cast<long long>(s.tiles) * p.a.Hkv * p.NR;
-            if (pos < base + w) break;
-            base += w;
-            ++b;
-        }
+    long long pos, hi;
+    int first;                     // sequence in which the part begins
+    Segment s;
+    __device__ Walker(const AttnParams& p, long long lo, long long end, long long base, int b) : pos(lo), hi(end), first(b) {
+        if (pos >= hi) return;
+        s.b = b;
+        s.len = cache_len_of(p, b);
+        s.tiles = tiles_of(s.len);
         const long long r = pos - base;
         const int it = static_cast<int>(r / s.tiles);
-        s.b = b;
-        s.hk = it / p.NR;
-        s.rg = it - s.hk * p.NR;
-        s.tile0 = static_cast<int>(r - static_cast<long long>(it) * s.tiles);
+        s.hk = it;
+        s.tile0 = s.tile1 = static_cast<int>(r - static_cast<long long>(it) * s.tiles);
+    }
+    __device__ __forceinline__ bool next(const AttnParams& p, const int* lens) {
+        if (pos >= hi) return false;
+        if (s.tile1 == s.tiles) {      // the item before is done
+            s.tile1 = 0;
+            if (++s.hk == p.a.Hkv) {
+                s.hk = 0;
+                ++s.b;
+                // (from shared memory: behind the busy memory system a load takes thousands of cycles)
+                const int i = s.b - first;
+                s.len = i < kLens ? lens[i] : cache_len_of(p, s.b);
+                s.tiles = tiles_of(s.len);
+            }
+        }
+        s.tile0 = s.tile1;
         const long long left = hi - pos;
         s.tile1 = s.tiles - s.tile0 <= left ? s.tiles : s.tile0 + static_cast<int>(left);
         pos += s.tile1 - s.tile0;
@@ -119,12 +137,15 @@ struct Walker {
 
 struct Control {
     uint64_t full[16], empty[16];
-    uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], aux, drain;
+    uint64_t s_full[3], p_full[3], pv_done[3], m_ready[4][2], pair[4], aux[2], q_full, drain;
     long long lo, hi, base, total, parts;
-    unsigned long long poison;     // drafted nodes with a V element that is not finite
+    unsigned long long poison[2];  // drafted nodes with a V element that is not finite (alternating)
     int b;
     uint32_t tmem;
     int abort;
+    int lens[kLens];
+    float ref[2][kTile];           // reference maxima after a tile, by its warpgroup
+    float sum[2][kTile];           // sums of the warpgroups at a segment's end
 };
 
 template <bool FP16>
@@ -138,56 +159,124 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// DP: head size padded to 64 or 128; R: row tiles per item; NS: stages of the ring (a K or a V tile each).
-template <bool FP16, int DP, int R>
+// The rare parts are kept out of line: with everything inlined the kernel was 120 KB of code, and its few
+// busy warps waited for instructions.
+
+// A wait that did not end at once.  One that runs out ends the call's work in this CTA, with the error
+// recorded.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+    const bool done = !*abort && mbar_wait_bounded(bar, parity, kWaitNs);
+    if (__all_sync(0xffffffffu, done)) return true;
+    if (!*abort) set_device_error(status, SVD_ERR_TIMEOUT);
+    *abort = 1;
+    return false;
+}
+
+// Adds to columns [d0, d1) of a written row what was taken out of V: for every visible node with infinities
+// or NaN, its weight times them.  `m` is the reference of the row's weights, `factor` what its sums were
+// multiplied by.
+template <bool FP16, class Out>
+__device__ __noinline__ void add_not_finite(const AttnParams& p, unsigned long long nodes, int b, int hk, size_t qrow, float m,
+                                            float factor, Out* to, int d0, int d1) {
+    const svd_tree_attention_args& a = p.a;
+    const uint16_t* qr = static_cast<const uint16_t*>(a.q) + qrow * a.D;
+    for (; nodes; nodes &= nodes - 1) {
+        const int i = __ffsll(static_cast<long long>(nodes)) - 1;
+        const size_t at = ((static_cast<size_t>(b) * a.n + i) * a.Hkv + hk) * a.D;
+        const uint16_t* kr = static_cast<const uint16_t*>(a.k_new) + at;
+        const uint16_t* vr = static_cast<const uint16_t*>(a.v_new) + at;
+        float dot = 0.f;
+#pragma unroll 1
+        for (int d = 0; d < a.D; ++d) dot += to_f32<FP16>(qr[d]) * to_f32<FP16>(kr[d]);
+        dot = p.qzero ? 0.f : (p.qflip ? -dot : dot);
+        // (a weight that underflows is not zero)
+        const float w = fmaxf(fast_exp2((dot - m) * p.c) * factor, 1e-30f);
+#pragma unroll 1
+        for (int d = d0; d < d1; ++d) {
+            const float x = to_f32<FP16>(vr[d]);
+            if (isfinite(x)) continue;
+            if (sizeof(Out) == 4) {
+                to[d] = static_cast<Out>(static_cast<float>(to[d]) + w * x);
+            } else {
+                const float y = to_f32<FP16>(static_cast<uint16_t>(to[d])) + w * x;
+                to[d] = static_cast<Out>(pack2<FP16>(y, y) & 0xffffu);
+            }
+        }
+    }
+}
+
+// Columns of S that do not count, 32 at `at`, become -inf.
+__device__ __noinline__ void hide_columns(uint32_t at, uint32_t keep) {
+    uint32_t x[32];
+    tmem_ld32(at, x);
+    tmem_wait_ld();
+    tmem_pin(x);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = keep >> e & 1u ? x[e] : 0xff800000u;
+    tmem_st32(at, x);
+    tmem_wait_st();
+}
+
+// DP: head size padded to 64 or 128.
+template <bool FP16, int DP>
 struct Shape {
     static constexpr int kHalves = DP / 64;
     static constexpr int kTileBytes = kTile * DP * 2;
-    static constexpr int kStages = R == 1 ? (DP == 128 ? 6 : 12) : (DP == 128 ? 5 : 10);
-    static constexpr int kSmem = R * kTileBytes + kStages * kTileBytes + 1024 + static_cast<int>(sizeof(Control));
-    static constexpr int kSoftmaxWarps = 4 * R;
+    static constexpr int kStages = DP == 128 ? 6 : 12;   // of the ring, a K or a V tile each
+    static constexpr int kSmem = (1 + kStages) * kTileBytes + static_cast<int>(sizeof(Control));
+    static constexpr int kSoftmaxWarps = 8;
     static constexpr int kThreads = 32 * (kSoftmaxWarps + 2);
     static_assert(kStages <= 16 && kSmem <= 232448, "shared memory");
 };
 
-template <bool FP16, int DP, int R>
-__global__ void __launch_bounds__(Shape<FP16, DP, R>::kThreads, 1)
+template <bool FP16, int DP>
+__global__ void __launch_bounds__(Shape<FP16, DP>::kThreads, 1)
 tree_attention_kernel(const __grid_constant__ AttnParams p) {
-    using Sh = Shape<FP16, DP, R>;
+    using Sh = Shape<FP16, DP>;
     constexpr int kHalves = Sh::kHalves, NS = Sh::kStages, kHalfBytes = kTile * 128;
-    extern __shared__ uint8_t dyn[];
-    uint8_t* sm = dyn + ((1024u - (smem_addr(dyn) & 1023u)) & 1023u);
-    uint8_t* sm_q = sm;
-    uint8_t* sm_kv = sm + R * Sh::kTileBytes;
+    // swizzled tiles begin at multiples of 1024 bytes; there is no static shared memory in front
+    extern __shared__ __align__(1024) uint8_t dyn[];
+    if (smem_addr(dyn) & 1023u) {
+        if (threadIdx.x == 0) set_device_error(p.status, SVD_ERR_CUDA);
+        return;
+    }
+    uint8_t* sm_q = dyn;
+    uint8_t* sm_kv = dyn + Sh::kTileBytes;
     Control& ctl = *reinterpret_cast<Control*>(sm_kv + NS * Sh::kTileBytes);
     const svd_tree_attention_args& a = p.a;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     constexpr int kProducer = Sh::kSoftmaxWarps, kMma = Sh::kSoftmaxWarps + 1;
-    volatile int* abort = &ctl.abort;
+    volatile int* const abort = &ctl.abort;
+    const int part = blockIdx.x / p.NR, rg = blockIdx.x % p.NR;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == kMma) {
         if (lane == 0) {
             for (int i = 0; i < NS; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 3; ++i) {
                 mbar_init(&ctl.s_full[i], 1);
                 mbar_init(&ctl.p_full[i], 4);
                 mbar_init(&ctl.pv_done[i], 1);
-                mbar_init(&ctl.q_full[i], 4);
             }
-            mbar_init(&ctl.aux, 1);
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(&ctl.m_ready[i][0], 1);
+                mbar_init(&ctl.m_ready[i][1], 1);
+                mbar_init(&ctl.pair[i], 2);
+            }
+            mbar_init(&ctl.aux[0], 1);
+            mbar_init(&ctl.aux[1], 1);
+            mbar_init(&ctl.q_full, 8);
             mbar_init(&ctl.drain, 1);
             fence_mbar_init();
             ctl.abort = 0;
-            ctl.poison = 0;
         }
         tmem_alloc(&ctl.tmem, 512);
     } else if (warp == kProducer) {
         if (lane == 0) { prefetch_map(&p.ck); prefetch_map(&p.cv); prefetch_map(&p.nk); prefetch_map(&p.nv); }
     } else if (warp == 0) {
         // this CTA's part of the line of tiles, and the sequence in which it begins
-        const long long HR = static_cast<long long>(a.Hkv) * p.NR;
+        const long long HR = a.Hkv;
         long long total = 0;
         bool bad = false;
         for (int b = lane; b < a.B; b += 32) {
@@ -199,8 +288,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         total *= HR;
-        const long long parts = total < static_cast<long long>(gridDim.x) ? total : gridDim.x;
-        const long long me = blockIdx.x;
+        const long long most = max_parts(p.NR), parts = total < most ? total : most, me = part;
         const long long lo = me < parts ? me * total / parts : 0, hi = me < parts ? (me + 1) * total / parts : 0;
         long long base = 0;
         int b0 = 0;
@@ -221,6 +309,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
             }
             base += __shfl_sync(0xffffffffu, x, 31);
         }
+        for (int i = lane; i < kLens; i += 32) ctl.lens[i] = b0 + i < a.B ? cache_len_of(p, b0 + i) : 0;
         if (lane == 0) {
             ctl.lo = lo;
             ctl.hi = hi;
@@ -234,30 +323,54 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
-    Walker wk = {ctl.lo, ctl.hi, ctl.base, ctl.b};
-    Segment s;
-    // Whole warps wait; the answer is the same in every lane.  A wait that runs out ends the call's
-    // work in this CTA with the error recorded.
+    Walker wk(p, ctl.lo, ctl.hi, ctl.base, ctl.b);
+    const Segment& s = wk.s;
+    // Whole warps wait; the answer is the same in every lane.
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool done = !*abort && mbar_wait_bounded(bar, parity & 1u, kWaitNs);
-        if (__all_sync(0xffffffffu, done)) return true;
-        if (!*abort) set_device_error(p.status, SVD_ERR_TIMEOUT);
-        *abort = 1;
-        return false;
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)) || wait_on(bar, parity & 1u, &ctl.abort, p.status);
     };
 
     if (warp == kProducer) {
         // ------------------------------------------------------------------ producer
-        uint32_t cnt = 0;   // tiles put into the ring
+        // V of a tile is needed only when its softmax is done, so it follows K of the next tile
+        struct Tile {
+            int page, row, hk, b;       // lane's page and row in it (row < 0: the drafted tile)
+        };
+        uint32_t cnt = 0, tiles = 0;    // loads and tiles so far
+        Tile before = {-1, -1, 0, 0};
         bool ok = true;
-        PartInfo inf = {0, 0, 0, -1};   // the item that starts here and goes on in later parts
-        while (ok && wk.next(p, s)) {
+        auto load = [&](const Tile& g, const CUtensorMap& cached, const CUtensorMap& drafted) {
+            const uint32_t st = cnt % NS;
+            if (cnt >= NS && !wait(&ctl.empty[st], cnt / NS - 1)) return false;
+            ++cnt;
+            uint8_t* dst = sm_kv + st * Sh::kTileBytes;
+            if (g.row >= 0) {
+                const uint32_t box = p.page_rows * 128u;
+                const int boxes = __popc(__ballot_sync(0xffffffffu, g.page >= 0));
+                if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], boxes * kHalves * box);
+                __syncwarp();
+                if (g.page >= 0) {
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
+                        tma_load_4d(dst + h * kHalfBytes + lane * box, &cached, h * 64, g.hk, g.row, g.page, &ctl.full[st]);
+                }
+            } else if (lane == 0) {
+                mbar_arrive_expect_tx(&ctl.full[st], kHalves * p.nb * 128u);
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h)
+                    tma_load_4d(dst + h * kHalfBytes, &drafted, h * 64, g.hk, 0, g.b, &ctl.full[st]);
+            }
+            __syncwarp();
+            return true;
+        };
+        PartInfo inf = {0, 0, -1};   // the item that starts here and goes on in later parts
+        while (ok && wk.next(p, ctl.lens)) {
             if (s.tile0 == 0 && s.tile1 < s.tiles) {
                 const long long end = wk.pos + (s.tiles - s.tile1);   // first tile behind the item
                 long long c = (end - 1) * ctl.parts / ctl.total;
                 while ((c + 1) * ctl.total / ctl.parts < end) ++c;
                 while (c * ctl.total / ctl.parts >= end) --c;
-                inf = PartInfo{s.b, s.hk, s.rg, static_cast<int>(c)};
+                inf = PartInfo{s.b, s.hk, static_cast<int>(c)};
             }
             const int pages_per_tile = kTile / p.page_rows;
             const int32_t* table = a.page_table + static_cast<size_t>(s.b) * a.max_pages;
@@ -275,34 +388,14 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
             int pg = page_of(s.tile0);
             for (int tile = s.tile0; ok && tile < s.tile1; ++tile) {
                 const int next_pg = tile + 1 < s.tile1 ? page_of(tile + 1) : -1;
-                const int boxes = __popc(__ballot_sync(0xffffffffu, pg >= 0));
-                for (int kv = 0; kv < 2; ++kv, ++cnt) {
-                    const int st = cnt % NS;
-                    if (cnt >= NS) ok = wait(&ctl.empty[st], cnt / NS - 1);
-                    if (!ok) break;
-                    uint8_t* dst = sm_kv + st * Sh::kTileBytes;
-                    if (tile < ctiles) {
-                        const uint32_t box = p.page_rows * 128u;
-                        if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], boxes * kHalves * box);
-                        __syncwarp();
-                        if (pg >= 0) {
-                            const int row = (tile * kTile + lane * p.page_rows) & (a.page_size - 1);
-#pragma unroll
-                            for (int h = 0; h < kHalves; ++h)
-                                tma_load_4d(dst + h * kHalfBytes + lane * box, kv ? &p.cv : &p.ck, h * 64, s.hk, row, pg,
-                                            &ctl.full[st]);
-                        }
-                    } else if (lane == 0) {
-                        mbar_arrive_expect_tx(&ctl.full[st], kHalves * p.nb * 128u);
-#pragma unroll
-                        for (int h = 0; h < kHalves; ++h)
-                            tma_load_4d(dst + h * kHalfBytes, kv ? &p.nv : &p.nk, h * 64, s.hk, 0, s.b, &ctl.full[st]);
-                    }
-                    __syncwarp();
-                }
+                const Tile now = {pg, tile < ctiles ? (tile * kTile + lane * p.page_rows) & (a.page_size - 1) : -1, s.hk, s.b};
+                ok = load(now, p.ck, p.nk);
+                if (ok && tiles++ > 0) ok = load(before, p.cv, p.nv);
+                before = now;
                 pg = next_pg;
             }
         }
+        if (ok && tiles > 0) load(before, p.cv, p.nv);
         if (lane == 0) p.info[blockIdx.x] = inf;
         // after a wait that ran out: no copy of this CTA may be in flight when it ends
         if (*abort)
@@ -312,297 +405,333 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         // ------------------------------------------------------------------ matrix instructions
         constexpr uint32_t kIdS = mma_desc(FP16, false, kTile, kTile), kIdO = mma_desc(FP16, true, kTile, DP);
         const uint32_t id_new = mma_desc(FP16, false, kTile, p.nb);
-        uint32_t tg = 0, unit = 0, seg = 0, naux = 0;   // tiles, units (tile x row tile), segments so far
+        // Tiles are numbered through the part.  S of the next tile is issued before O of this one; the first S
+        // of a segment, which waits for its Q, behind the last O of the one before.
         bool ok = true;
-        while (ok && wk.next(p, s)) {
-            const int nt = s.tile1 - s.tile0, nu = nt * R;
-            const uint32_t u0 = unit, t0 = tg;
-            auto issue_s = [&](uint32_t u) {   // u: unit within the segment
-                const uint32_t slot = (u0 + u) & 1u, r = R == 2 ? (u & 1u) : 0u, tile = u / R;
-                const uint32_t cnt = 2 * (t0 + tile), st = cnt % NS;
-                if (u0 + u >= 2) ok = ok && wait(&ctl.pv_done[slot], (u0 + u - 2) >> 1);
-                if (r == 0) ok = ok && wait(&ctl.full[st], cnt / NS);
-                if (tile == 0) ok = ok && wait(&ctl.q_full[r], seg);
-                if (!ok) return;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t q = smem_addr(sm_q + r * Sh::kTileBytes), k = smem_addr(sm_kv + st * Sh::kTileBytes);
-                    const uint32_t id = s.tile0 + static_cast<int>(tile) == s.tiles - 1 ? id_new : kIdS;
+        const bool one = lane == 0;
+        const uint64_t q_desc = mat_desc(smem_addr(sm_q), 16, 1024);
+        const uint32_t n_tiles = static_cast<uint32_t>(ctl.hi - ctl.lo);
+        uint32_t u = 0, naux = 0, seg = 0;
+        auto issue_s = [&](uint32_t w, bool drafted) {
+            const uint32_t cnt = w == 0 ? 0 : 2 * w - 1, st = cnt % NS, slot = w % 3;   // (in the producer's order)
+            if (w >= 3) ok = ok && wait(&ctl.pv_done[slot], w / 3 - 1);
+            ok = ok && wait(&ctl.full[st], cnt / NS);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t k_desc = mat_desc(smem_addr(sm_kv + st * Sh::kTileBytes), 16, 1024);
+            const uint32_t id = drafted ? id_new : kIdS;
 #pragma unroll
-                    for (int kk = 0; kk < DP / 16; ++kk) {
-                        const uint32_t off = (kk / 4) * kHalfBytes + (kk % 4) * 32;
-                        mma_ss(tmem + slot * kTile, mat_desc(q + off, 16, 1024), mat_desc(k + off, 16, 1024), id, kk > 0);
-                    }
-                    mma_commit(&ctl.s_full[slot]);
-                    if (r == R - 1) mma_commit(&ctl.empty[st]);
-                }
-                __syncwarp();
-            };
-            issue_s(0);
-            for (uint32_t u = 0; ok && u < static_cast<uint32_t>(nu); ++u) {
-                if (u + 1 < static_cast<uint32_t>(nu)) issue_s(u + 1);
-                if (!ok) break;
-                const uint32_t slot = (u0 + u) & 1u, r = R == 2 ? (u & 1u) : 0u, tile = u / R;
-                const uint32_t cnt = 2 * (t0 + tile) + 1, st = cnt % NS;
+            for (int kk = 0; kk < DP / 16; ++kk) {
+                const uint32_t off = ((kk / 4) * kHalfBytes + (kk % 4) * 32) >> 4;   // (of the address fields)
+                mma_ss(one, tmem + slot * kTile, q_desc + off, k_desc + off, id, kk > 0);
+            }
+            mma_commit(one, &ctl.s_full[slot]);
+            mma_commit(one, &ctl.empty[st]);
+            __syncwarp();
+        };
+        while (ok && wk.next(p, ctl.lens)) {
+            ok = wait(&ctl.q_full, seg++);
+            for (int kt = s.tile0 - 1; ok && kt < s.tile1; ++kt) {
+                // (one place for the code: the round at tile0 - 1 only starts the first S)
+                if (kt + 1 < s.tile1) issue_s(u + (kt >= s.tile0 ? 1 : 0), kt + 1 == s.tiles - 1);
+                if (!ok || kt < s.tile0) continue;
+                const uint32_t cnt = u + 1 == n_tiles ? 2 * u + 1 : 2 * u + 2, st = cnt % NS, slot = u % 3;
                 uint8_t* v = sm_kv + st * Sh::kTileBytes;
-                const int kt = s.tile0 + static_cast<int>(tile);
                 const bool drafted = kt == s.tiles - 1;
                 const int valid = drafted ? p.nb : min(kTile, s.len - kt * kTile);
                 const int steps = (valid + 15) >> 4;
-                if (r == 0) {
-                    ok = wait(&ctl.full[st], cnt / NS);
-                    if (!ok) break;
-                    if (drafted) {
-                        // rows of padding nodes become zero; elements that are not finite are taken out
-                        // and their nodes noted (rows behind n came as zeros from the TMA unit)
-                        const int used = a.n_nodes ? max(0, min(a.n, __ldg(a.n_nodes + s.b))) : a.n;
-                        const uint32_t ex = FP16 ? 0x7c00u : 0x7f80u;
-                        unsigned long long bad = 0;
-                        for (int i = lane; i < a.n * (DP / 8); i += 32) {
-                            const int row = i / (DP / 8), ch = i % (DP / 8);
-                            uint4* at = reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-                            if (row >= used) {
-                                *at = make_uint4(0, 0, 0, 0);
-                                continue;
-                            }
-                            uint4 x = *at;
-                            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-                            bool hit = false;
+                ok = wait(&ctl.full[st], cnt / NS);
+                if (!ok) break;
+                if (drafted) {
+                    // rows of padding nodes become zero; elements that are not finite are taken out
+                    // and their nodes noted (rows behind n came as zeros from the TMA unit)
+                    const int used = a.n_nodes ? max(0, min(a.n, __ldg(a.n_nodes + s.b))) : a.n;
+                    const uint32_t ex = FP16 ? 0x7c00u : 0x7f80u;
+                    unsigned long long bad = 0;
+#pragma unroll 2
+                    for (int i = lane; i < a.n * (DP / 8); i += 32) {
+                        const int row = i / (DP / 8), ch = i % (DP / 8);
+                        uint4* at = reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + row * 128 +
+                                                             (((ch & 7) ^ (row & 7)) << 4));
+                        uint4 x = *at;
+                        uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+                        bool hit = false;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if ((w[e] & ex) == ex) { w[e] &= 0xffff0000u; hit = true; }
-                                if ((w[e] & (ex << 16)) == (ex << 16)) { w[e] &= 0x0000ffffu; hit = true; }
-                            }
-                            if (hit) {
-                                *at = x;
-                                bad |= 1ull << row;
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            const bool lo = (w[e] & ex) == ex, hi = (w[e] & (ex << 16)) == (ex << 16);
+                            w[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+                            hit = hit || lo || hi;
                         }
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-                        if (lane == 0) {
-                            ctl.poison = bad;
-                            mbar_arrive(&ctl.aux);
-                        }
-                        ++naux;
-                        fence_async();
-                        __syncwarp();
-                    } else if (valid < steps * 16) {
-                        for (int i = lane; i < (steps * 16 - valid) * kHalves * 8; i += 32) {
-                            const int row = valid + i / (kHalves * 8), ch = i % (kHalves * 8);
-                            *reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + row * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_async();
-                        __syncwarp();
+                        if (row >= used) x = make_uint4(0, 0, 0, 0);
+                        else if (hit) bad |= 1ull << row;
+                        if (hit || row >= used) *at = x;
                     }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+                    if (lane == 0) {
+                        ctl.poison[naux & 1u] = bad;
+                        mbar_arrive(&ctl.aux[naux & 1u]);
+                    }
+                    ++naux;
+                    fence_async();
+                    __syncwarp();
+                } else if (valid < steps * 16) {
+                    for (int i = lane; i < (steps * 16 - valid) * kHalves * 8; i += 32) {
+                        const int row = valid + i / (kHalves * 8), ch = i % (kHalves * 8);
+                        *reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + row * 128 + ((ch & 7) << 4)) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async();
+                    __syncwarp();
                 }
-                ok = wait(&ctl.p_full[slot], (u0 + u) >> 1);
+                ok = wait(&ctl.p_full[slot], u / 3);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t vb = smem_addr(v);
-                    for (int kk = 0; kk < steps; ++kk)
-                        mma_ts(tmem + 256 + r * DP, tmem + slot * kTile + kk * 8, mat_desc(vb + kk * 2048, kHalfBytes, 1024), kIdO,
-                               tile > 0 || kk > 0);
-                    mma_commit(&ctl.pv_done[slot]);
-                    if (r == R - 1) mma_commit(&ctl.empty[st]);
+                const uint64_t v_desc = mat_desc(smem_addr(v), kHalfBytes, 1024);
+                auto step = [&](int kk) {
+                    mma_ts(one, tmem + 3 * kTile, tmem + slot * kTile + kk * 8, v_desc + (kk * 2048 >> 4), kIdO,
+                           kt > s.tile0 || kk > 0);
+                };
+                if (steps == kTile / 16) {
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk) step(kk);
+                } else {
+#pragma unroll 1
+                    for (int kk = 0; kk < steps; ++kk) step(kk);
                 }
+                mma_commit(one, &ctl.pv_done[slot]);
+                mma_commit(one, &ctl.empty[st]);
                 __syncwarp();
+                ++u;
             }
-            unit += nu;
-            tg += nt;
-            ++seg;
         }
         // nothing may be in flight when TMEM is freed
-        if (lane == 0) mma_commit(&ctl.drain);
+        mma_commit(one, &ctl.drain);
+        __syncwarp();
         mbar_wait_bounded(&ctl.drain, 0, kWaitNs);
-        (void)naux;
     } else {
         // ------------------------------------------------------------------ softmax: thread = row
-        const int rt = warp >> 2, trow = (warp & 3) * 32 + lane;
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t o_at = lane_base + 256 + rt * DP;
+        // warpgroup wg takes the tiles with number % 2 == wg, and half of O's columns at a segment's end
+        const uint32_t wg = warp >> 2;
+        const int quarter = warp & 3, trow = quarter * 32 + lane;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t o_at = lane_base + 3 * kTile;
         const float c = p.c;
-        uint32_t unit = rt, seg = 0, naux = 0;
+        const int row = rg * kTile + trow;                       // row of the key head: node * G + head
+        const bool live = row < p.rows, warp_live = rg * kTile + quarter * 32 < p.rows;
+        const int node = live ? row / p.G : 0, g_head = live ? row - node * p.G : 0;
+        uint32_t u = 0, naux = 0, phase = 0;                     // tiles, drafted tiles, exchanges so far
         bool ok = true;
-        while (ok && wk.next(p, s)) {
-            const int in_item = rt * kTile + trow;                   // row within the item
-            const int row = s.rg * R * kTile + in_item;              // row of the key head: node * G + head
-            const bool live = row < p.rows;
-            const bool warp_live = s.rg * R * kTile + rt * kTile + (warp & 3) * 32 < p.rows;
-            const int node = live ? row / p.G : 0;
-            const int head = s.hk * p.G + (live ? row - node * p.G : 0);
-            const int used = a.n_nodes ? max(0, min(a.n, __ldg(a.n_nodes + s.b))) : a.n;
-            const size_t qrow = (static_cast<size_t>(s.b) * a.n + node) * a.Hq + head;
-            if (warp_live) {
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + qrow * a.D);
-                uint8_t* dst = sm_q + rt * Sh::kTileBytes + trow * 128;
-                uint4 x[DP / 8];
-#pragma unroll
-                for (int ch = 0; ch < DP / 8; ++ch)
-                    x[ch] = live && ch * 8 < a.D && !p.qzero ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
-                const uint32_t flip = p.qflip ? 0x80008000u : 0u;
-#pragma unroll
-                for (int ch = 0; ch < DP / 8; ++ch) {
-                    x[ch].x ^= flip; x[ch].y ^= flip; x[ch].z ^= flip; x[ch].w ^= flip;
-                    *reinterpret_cast<uint4*>(dst + (ch >> 3) * kHalfBytes + (((ch & 7) ^ (trow & 7)) << 4)) = x[ch];
-                }
-                fence_async();
+        auto q_row = [&](const Segment& g) { return (static_cast<size_t>(g.b) * a.n + node) * a.Hq + g.hk * p.G + g_head; };
+        // Q rows of a segment into shared memory (this warpgroup: its half of the columns), completed by q_ready
+        auto q_chunk = [&](int i) {
+            const int ch = static_cast<int>(wg) * (DP / 16) + i;
+            return sm_q + trow * 128 + (ch >> 3) * kHalfBytes + (((ch & 7) ^ (trow & 7)) << 4);
+        };
+        auto fetch_q = [&](const Segment& g) {
+            const uint16_t* src = static_cast<const uint16_t*>(a.q) + q_row(g) * a.D;
+#pragma unroll 1
+            for (int i = 0; i < DP / 16; ++i) {
+                const int ch = static_cast<int>(wg) * (DP / 16) + i;
+                // (of zero bytes from global memory the rest is zeros)
+                const uint32_t bytes = live && ch * 8 < a.D && !p.qzero ? 16u : 0u;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(q_chunk(i))), "l"(src + (bytes ? ch * 8 : 0)),
+                             "r"(bytes)
+                             : "memory");
             }
+        };
+        auto q_ready = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (p.qflip) {
+#pragma unroll 1
+                for (int i = 0; i < DP / 16; ++i) {
+                    uint4* at = reinterpret_cast<uint4*>(q_chunk(i));
+                    uint4 x = *at;
+                    x.x ^= 0x80008000u; x.y ^= 0x80008000u; x.z ^= 0x80008000u; x.w ^= 0x80008000u;
+                    *at = x;
+                }
+            }
+            fence_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.q_full[rt]);
+            if (lane == 0) mbar_arrive(&ctl.q_full);
+        };
+        // `wk` is at the segment behind the current one
+        bool more = wk.next(p, ctl.lens);
+        if (more) {
+            fetch_q(wk.s);
+            q_ready();
+        }
+        int seq = -1, anc_seq = -1, used = a.n;   // sequences that `used` and `anc` belong to
+        unsigned long long anc = 0;
+        while (ok && more) {
+            const Segment s = wk.s;
+            more = wk.next(p, ctl.lens);
+            if (a.n_nodes && s.b != seq) used = max(0, min(a.n, __ldg(a.n_nodes + s.b)));
+            seq = s.b;
             // ancestors of this row's node, by shuffles of the sequence's parents
-            unsigned long long anc = 0;
             const bool has_new = s.tile1 == s.tiles;
-            if (has_new && warp_live) {
+            if (has_new && warp_live && s.b != anc_seq) {
                 const size_t at = static_cast<size_t>(s.b) * a.n;
                 const int p0 = lane < a.n ? checked_parent(a.parent, at, lane, p.status) : -1;
                 const int p1 = lane + 32 < a.n ? checked_parent(a.parent, at, lane + 32, p.status) : -1;
                 int i = live && node < used ? node : -1;
+                anc = 0;
                 while (__any_sync(0xffffffffu, i >= 0)) {
                     if (i >= 0) anc |= 1ull << i;
                     const int q0 = __shfl_sync(0xffffffffu, p0, i & 31), q1 = __shfl_sync(0xffffffffu, p1, i & 31);
                     i = i < 0 ? -1 : (i < 32 ? q0 : q1);
                 }
+                anc_seq = s.b;
             }
+            // m: the reference that this thread's l is relative to
             float m = -INFINITY, l = 0.f;
-            for (int kt = s.tile0; ok && kt < s.tile1; ++kt, unit += R) {
-                const uint32_t slot = unit & 1u;
-                ok = wait(&ctl.s_full[slot], unit >> 1);
+            const uint32_t u_end = u + static_cast<uint32_t>(s.tile1 - s.tile0);
+            for (int kt = s.tile0; ok && kt < s.tile1; ++kt, ++u) {
+                // the last S of this segment is there: Q is free for the next one
+                const bool last = kt + 1 == s.tile1, mine = (u & 1u) == wg;
+                const uint32_t slot = u % 3;
+                if (mine || (last && more)) ok = wait(&ctl.s_full[slot], u / 3);
                 if (!ok) break;
-                if (warp_live) {
+                if (last && more) fetch_q(wk.s);
+                if (mine && warp_live) {
                     tc_fence_after();
                     const uint32_t s_at = lane_base + slot * kTile;
-                    auto tile = [&](auto nch_tag, auto mask) {
-                        constexpr int NC = decltype(nch_tag)::value;   // chunks of 32 columns
-                        uint32_t x[NC][32];
-#pragma unroll
-                        for (int q = 0; q < NC; ++q) tmem_ld32(s_at + q * 32, x[q]);
+                    // Chunks of 32 columns, two in each round of a loop that is kept short: with the tile
+                    // unrolled the warps waited for instructions (2.9 of 8 stalled cycles an issue).
+                    const bool drafted = kt == s.tiles - 1;
+                    const int rounds = drafted ? 1 : 2, valid = s.len - kt * kTile;
+                    if (drafted || valid < kTile) {
+#pragma unroll 1
+                        for (int q = 0; q < 2 * rounds; ++q) {
+                            const int left = valid - 32 * q;
+                            hide_columns(s_at + q * 32, drafted ? static_cast<uint32_t>(anc >> (32 * q))
+                                                                : (left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u)));
+                        }
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    uint32_t x[2][32];
+#pragma unroll 1
+                    for (int q = 0; q < rounds; ++q) {
+                        tmem_ld32(s_at + q * 64, x[0]);
+                        tmem_ld32(s_at + q * 64 + 32, x[1]);
                         tmem_wait_ld();
-                        mask(x);
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int q = 0; q < NC; ++q)
+                        for (int h = 0; h < 2; ++h) {
+                            tmem_pin(x[h]);
 #pragma unroll
                             for (int e = 0; e < 32; e += 8)
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    mx[k] = fmax3(mx[k], __uint_as_float(x[q][e + 2 * k]), __uint_as_float(x[q][e + 2 * k + 1]));
-                        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                        if (kt == s.tile0) {
-                            m = mt;
-                        } else {
-                            const bool up = !(mt <= m + p.thr);
-                            if (__any_sync(0xffffffffu, up)) {
-                                // the last product into this O has to be complete
-                                const uint32_t prev = unit - R;
-                                ok = wait(&ctl.pv_done[prev & 1u], prev >> 1);
-                                if (!ok) return;
-                                tc_fence_after();
-                                const float mn = up ? fmaxf(m, mt) : m;
-                                const float f = up ? fast_exp2((m - mn) * c) : 1.f;
-                                m = mn;
-                                l *= f;
+                                    mx[k] = fmax3(mx[k], __uint_as_float(x[h][e + 2 * k]), __uint_as_float(x[h][e + 2 * k + 1]));
+                        }
+                    }
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    // the first chunk comes back while the reference is settled
+                    tmem_ld32(s_at, x[0]);
+                    float mn = mt;
+                    if (kt > s.tile0) {
+                        const uint32_t prev = u - 1;
+                        ok = wait(&ctl.m_ready[quarter][prev & 1u], prev >> 1);
+                        const float mp = *const_cast<volatile float*>(&ctl.ref[prev & 1u][trow]);
+                        const bool up = !(mt <= mp + p.thr);
+                        mn = up ? fmaxf(mp, mt) : mp;
+                        if (__any_sync(0xffffffffu, up)) {
+                            // every product into O so far has to be complete
+                            ok = ok && wait(&ctl.pv_done[prev % 3], prev / 3);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const float f = up ? fast_exp2((mp - mn) * c) : 1.f;
 #pragma unroll 1
-                                for (int q = 0; q < DP / 32; ++q) {
-                                    uint32_t o[32];
-                                    tmem_ld32(o_at + q * 32, o);
-                                    tmem_wait_ld();
+                            for (int q = 0; q < DP / 32; ++q) {
+                                uint32_t o[32];
+                                tmem_ld32(o_at + q * 32, o);
+                                tmem_wait_ld();
+                                tmem_pin(o);
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                    tmem_st32(o_at + q * 32, o);
-                                }
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st32(o_at + q * 32, o);
                             }
                         }
-                        const float mref = m == -INFINITY ? 0.f : -m * c;
-                        const float2 c2 = make_float2(c, c), m2 = make_float2(mref, mref);
-                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    }
+                    ctl.ref[wg][trow] = mn;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.m_ready[quarter][wg]);
+                    if (__any_sync(0xffffffffu, m != mn)) l *= m == mn ? 1.f : fast_exp2((m - mn) * c);
+                    m = mn;
+                    const float mref = m == -INFINITY ? 0.f : -m * c;
+                    const float2 c2 = make_float2(c, c), m2 = make_float2(mref, mref);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                    for (int q = 0; q < rounds; ++q) {
 #pragma unroll
-                        for (int q = 0; q < NC; ++q) {
+                        for (int h = 0; h < 2; ++h) {
+                            tmem_wait_ld();
+                            tmem_pin(x[h]);
+                            // the next chunk's load; P goes over columns that have been read
+                            if (h == 0 || q + 1 < rounds) tmem_ld32(s_at + (2 * q + h + 1) * 32, x[h ^ 1]);
                             uint32_t w[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                float2 y = fma2(make_float2(__uint_as_float(x[q][2 * e]), __uint_as_float(x[q][2 * e + 1])), c2, m2);
-                                y.x = fast_exp2(y.x);
-                                y.y = fast_exp2(y.y);
-                                sum[e & 1] = add2(sum[e & 1], y);
-                                w[e] = pack2<FP16>(y.x, y.y);
+                                float2 z = fma2(make_float2(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1])), c2, m2);
+                                z.x = fast_exp2(z.x);
+                                z.y = fast_exp2(z.y);
+                                sum[e & 1] = add2(sum[e & 1], z);
+                                w[e] = pack2<FP16>(z.x, z.y);
                             }
-                            tmem_st16(s_at + q * 16, w);
+                            tmem_st16(s_at + (2 * q + h) * 16, w);
                         }
-                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                        tmem_wait_st();
-                        tc_fence_before();
-                    };
-                    if (kt == s.tiles - 1) {
-                        tile(std::integral_constant<int, 2>{}, [&](uint32_t (&x)[2][32]) {
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const uint32_t bits = static_cast<uint32_t>(anc >> (32 * q));
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!(bits >> e & 1u)) x[q][e] = 0xff800000u;
-                            }
-                        });
-                    } else {
-                        const int valid = s.len - kt * kTile;
-                        tile(std::integral_constant<int, 4>{}, [&](uint32_t (&x)[4][32]) {
-                            if (valid < kTile) {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e)
-                                        if (q * 32 + e >= valid) x[q][e] = 0xff800000u;
-                            }
-                        });
                     }
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    tmem_wait_st();
+                    tc_fence_before();
                     if (!ok) break;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.p_full[slot]);
+                if (mine && lane == 0) mbar_arrive(&ctl.p_full[slot]);
+                if (last && more) q_ready();
             }
             if (!ok) break;
-            // ---- the segment's end: O of this row, normalised or as a part
-            const uint32_t prev = unit - R;
-            ok = wait(&ctl.pv_done[prev & 1u], prev >> 1);
-            if (has_new) ok = ok && wait(&ctl.aux, naux);
+            // ---- the segment's end: this warpgroup's columns of O, normalised or as a part
+            const uint32_t prev = u_end - 1;
+            ok = wait(&ctl.pv_done[prev % 3], prev / 3);
+            if (has_new) ok = ok && wait(&ctl.aux[naux & 1u], naux >> 1);
             if (!ok) break;
             tc_fence_after();
-            const unsigned long long poison = has_new ? *reinterpret_cast<volatile unsigned long long*>(&ctl.poison) & anc : 0ull;
+            const unsigned long long poison = has_new ? *const_cast<volatile unsigned long long*>(&ctl.poison[naux & 1u]) & anc : 0ull;
             if (has_new) ++naux;
             if (warp_live) {
+                // both warpgroups' sums, relative to the last tile's reference
+                ok = wait(&ctl.m_ready[quarter][prev & 1u], prev >> 1);
+                const float mf = *const_cast<volatile float*>(&ctl.ref[prev & 1u][trow]);
+                if (l != 0.f && m != mf) l *= fast_exp2((m - mf) * c);
+                m = mf;
+                ctl.sum[wg][trow] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.pair[quarter]);
+                ok = wait(&ctl.pair[quarter], phase++) && ok;
+                // (in this order in both warpgroups)
+                l = *const_cast<volatile float*>(&ctl.sum[0][trow]) + *const_cast<volatile float*>(&ctl.sum[1][trow]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.pair[quarter]);   // read: may be overwritten
+                ok = wait(&ctl.pair[quarter], phase++) && ok;
+                if (!ok) break;
+                const size_t qrow = q_row(s);
                 const bool whole = s.tile0 == 0 && s.tile1 == s.tiles;
-                const int slot = 2 * blockIdx.x + (s.tile0 == 0 ? 1 : 0);
+                const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (s.tile0 == 0 ? 1 : 0)) * p.used + trow;
                 const bool pad = node >= used;
-                const float inv = whole ? (pad || l == 0.f ? 0.f : __fdiv_rn(1.f, l)) : 1.f;
-                float* part = p.o + (static_cast<size_t>(slot) * p.used + in_item) * a.D;
+                const float inv = pad || l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+                float* to_part = p.o + slot * a.D;
                 uint16_t* out = static_cast<uint16_t*>(a.out) + qrow * a.D;
 #pragma unroll 1
-                for (int q = 0; q < DP / 32; ++q) {
+                for (int q = 0; q < DP / 64; ++q) {
+                    const int d0 = static_cast<int>(wg) * (DP / 2) + q * 32;
                     uint32_t o[32];
-                    tmem_ld32(o_at + q * 32, o);
+                    tmem_ld32(o_at + d0, o);
                     tmem_wait_ld();
-                    for (unsigned long long bits = poison; bits; bits &= bits - 1) {
-                        // a visible node with infinities or NaN: its weight, and what was taken out of its V
-                        const int i = __ffsll(static_cast<long long>(bits)) - 1;
-                        const size_t at = ((static_cast<size_t>(s.b) * a.n + i) * a.Hkv + s.hk) * a.D;
-                        const uint16_t* kr = static_cast<const uint16_t*>(a.k_new) + at;
-                        const uint16_t* vr = static_cast<const uint16_t*>(a.v_new) + at;
-                        const uint16_t* qr = static_cast<const uint16_t*>(a.q) + qrow * a.D;
-                        float dot = 0.f;
-                        for (int d = 0; d < a.D; ++d) dot += to_f32<FP16>(qr[d]) * to_f32<FP16>(kr[d]);
-                        dot = p.qzero ? 0.f : (p.qflip ? -dot : dot);
-                        const float w = fmaxf(fast_exp2((dot - m) * c), 1e-30f);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int d = q * 32 + e;
-                            const float x = d < a.D ? to_f32<FP16>(vr[d]) : 0.f;
-                            if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + w * x);
-                        }
-                    }
+                    tmem_pin(o);
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
-                        const int d = q * 32 + e;
+                        const int d = d0 + e;
                         if (!live || d >= a.D) continue;
                         float y[8];
 #pragma unroll
@@ -615,21 +744,29 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                             v.w = pad ? 0u : pack2<FP16>(y[6] * inv, y[7] * inv);
                             *reinterpret_cast<uint4*>(out + d) = v;
                         } else {
-                            *reinterpret_cast<float4*>(part + d) = make_float4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<float4*>(part + d + 4) = make_float4(y[4], y[5], y[6], y[7]);
+                            *reinterpret_cast<float4*>(to_part + d) = make_float4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<float4*>(to_part + d + 4) = make_float4(y[4], y[5], y[6], y[7]);
                         }
                     }
                     __syncwarp();
                 }
-                if (live) {
-                    if (!whole) p.ml[static_cast<size_t>(slot) * p.used + in_item] = make_float2(m, l);
+                if (live && poison) {
+                    const int d0 = static_cast<int>(wg) * (DP / 2), d1 = min(a.D, d0 + DP / 2);
+                    if (whole) add_not_finite<FP16>(p, poison, s.b, s.hk, qrow, m, inv, out, d0, d1);
+                    else add_not_finite<FP16>(p, poison, s.b, s.hk, qrow, m, 1.f, to_part, d0, d1);
+                }
+                __syncwarp();
+                if (live && wg == 0) {
+                    if (!whole) p.ml[slot] = make_float2(m, l);
                     else if (a.lse) a.lse[qrow] = pad ? -INFINITY : (m == -INFINITY ? 0.f : m * c * kLn2) + logf(l);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            ++seg;
         }
+        // (a wait that ran out may have left some in flight)
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        tmem_wait_ld();
     }
     tc_fence_before();
     __syncthreads();
@@ -645,12 +782,14 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
     const svd_tree_attention_args& a = p.a;
     const PartInfo inf = p.info[blockIdx.x];
     if (inf.last < 0) return;
-    const int lane = threadIdx.x & 31;
-    const int in_item = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
-    const int row = inf.rg * row_tiles(p.rows) * kTile + in_item;
-    if (in_item >= p.used || row >= p.rows) return;
-    const int first = blockIdx.x, parts = inf.last - first + 1;
-    auto slot = [&](int i) { return static_cast<size_t>(2 * (first + i) + (i == 0 ? 1 : 0)) * p.used + in_item; };
+    const int lane = threadIdx.x & 31, rg = blockIdx.x % p.NR;
+    const int in_group = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
+    const int row = rg * kTile + in_group;
+    if (in_group >= p.used || row >= p.rows) return;
+    const int parts = inf.last - static_cast<int>(blockIdx.x) / p.NR + 1;
+    auto slot = [&](int i) {
+        return (2 * (static_cast<size_t>(blockIdx.x) + static_cast<size_t>(i) * p.NR) + (i == 0 ? 1 : 0)) * p.used + in_group;
+    };
     float m = -INFINITY;
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.ml[slot(i)].x);
 #pragma unroll
@@ -711,12 +850,13 @@ bool encode(CUtensorMap* map, bool fp16, const void* base, int D, int Hkv, int r
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP16, int DP, int R>
+template <bool FP16, int DP>
 cudaError_t launch(const AttnParams& p, cudaStream_t st) {
-    using Sh = Shape<FP16, DP, R>;
-    cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<FP16, DP, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    using Sh = Shape<FP16, DP>;
+    cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<FP16, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
     if (e != cudaSuccess) return e;
-    tree_attention_kernel<FP16, DP, R><<<kCtas, Sh::kThreads, Sh::kSmem, st>>>(p);
+    const int ctas = p.NR * max_parts(p.NR);
+    tree_attention_kernel<FP16, DP><<<ctas, Sh::kThreads, Sh::kSmem, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
@@ -724,7 +864,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(kCtas, (p.used + kCombineWarps - 1) / kCombineWarps);
+    cfg.gridDim = dim3(ctas, (p.used + kCombineWarps - 1) / kCombineWarps);
     cfg.blockDim = dim3(kCombineWarps * 32);
     cfg.stream = st;
     cfg.attrs = attr;
@@ -734,9 +874,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
 
 template <bool FP16>
 cudaError_t launch_type(const AttnParams& p, cudaStream_t st) {
-    const bool wide = p.a.D > 64, two = row_tiles(p.rows) == 2;
-    if (wide) return two ? launch<FP16, 128, 2>(p, st) : launch<FP16, 128, 1>(p, st);
-    return two ? launch<FP16, 64, 2>(p, st) : launch<FP16, 64, 1>(p, st);
+    return p.a.D > 64 ? launch<FP16, 128>(p, st) : launch<FP16, 64>(p, st);
 }
 
 }  // namespace
@@ -749,9 +887,8 @@ int launch_tree_attention(const svd_tree_attention_args& a, void* ws, void* stre
     p.a = a;
     p.G = a.Hq / a.Hkv;
     p.rows = a.n * p.G;
-    const int group = row_tiles(p.rows) * kTile;
-    p.used = p.rows < group ? p.rows : group;
-    p.NR = (p.rows + group - 1) / group;
+    p.used = p.rows < kTile ? p.rows : kTile;
+    p.NR = row_groups(p.rows);
     p.page_rows = a.page_size < kTile ? a.page_size : kTile;
     while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
     p.nb = (a.n + 15) / 16 * 16;
