@@ -137,7 +137,7 @@ struct Walker {
 
 struct Control {
     uint64_t full[16], empty[16];
-    uint64_t s_full[3], p_full[3], pv_done[3], m_ready[4][2], pair[4], aux[2], q_full, drain;
+    uint64_t s_full[3], p_full[3], pv_done[3], m_ready[4][2], pair[4], aux[2], q_full, drain[2];
     long long lo, hi, base, total, parts;
     unsigned long long poison[2];  // drafted nodes with a V element that is not finite (alternating)
     int b;
@@ -225,7 +225,7 @@ struct Shape {
     static constexpr int kStages = DP == 128 ? 6 : 12;   // of the ring, a K or a V tile each
     static constexpr int kSmem = (1 + kStages) * kTileBytes + static_cast<int>(sizeof(Control));
     static constexpr int kSoftmaxWarps = 8;
-    static constexpr int kThreads = 32 * (kSoftmaxWarps + 2);
+    static constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
     static_assert(kStages <= 16 && kSmem <= 232448, "shared memory");
 };
 
@@ -245,13 +245,13 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
     Control& ctl = *reinterpret_cast<Control*>(sm_kv + NS * Sh::kTileBytes);
     const svd_tree_attention_args& a = p.a;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    constexpr int kProducer = Sh::kSoftmaxWarps, kMma = Sh::kSoftmaxWarps + 1;
+    constexpr int kProducer = Sh::kSoftmaxWarps, kMmaS = Sh::kSoftmaxWarps + 1, kMmaO = Sh::kSoftmaxWarps + 2;
     volatile int* const abort = &ctl.abort;
     const int part = blockIdx.x / p.NR, rg = blockIdx.x % p.NR;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (warp == kMma) {
+    if (warp == kMmaS) {
         if (lane == 0) {
             for (int i = 0; i < NS; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
             for (int i = 0; i < 3; ++i) {
@@ -267,7 +267,8 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
             mbar_init(&ctl.aux[0], 1);
             mbar_init(&ctl.aux[1], 1);
             mbar_init(&ctl.q_full, 8);
-            mbar_init(&ctl.drain, 1);
+            mbar_init(&ctl.drain[0], 1);
+            mbar_init(&ctl.drain[1], 1);
             fence_mbar_init();
             ctl.abort = 0;
         }
@@ -332,12 +333,12 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
 
     if (warp == kProducer) {
         // ------------------------------------------------------------------ producer
-        // V of a tile is needed only when its softmax is done, so it follows K of the next tile
+        // S is formed two tiles ahead of O, so V of a tile follows K of the second next one
         struct Tile {
             int page, row, hk, b;       // lane's page and row in it (row < 0: the drafted tile)
         };
         uint32_t cnt = 0, tiles = 0;    // loads and tiles so far
-        Tile before = {-1, -1, 0, 0};
+        Tile before = {-1, -1, 0, 0}, before2 = before;
         bool ok = true;
         auto load = [&](const Tile& g, const CUtensorMap& cached, const CUtensorMap& drafted) {
             const uint32_t st = cnt % NS;
@@ -390,52 +391,64 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                 const int next_pg = tile + 1 < s.tile1 ? page_of(tile + 1) : -1;
                 const Tile now = {pg, tile < ctiles ? (tile * kTile + lane * p.page_rows) & (a.page_size - 1) : -1, s.hk, s.b};
                 ok = load(now, p.ck, p.nk);
-                if (ok && tiles++ > 0) ok = load(before, p.cv, p.nv);
+                if (ok && tiles++ > 1) ok = load(before2, p.cv, p.nv);
+                before2 = before;
                 before = now;
                 pg = next_pg;
             }
         }
+        if (ok && tiles > 1) ok = load(before2, p.cv, p.nv);
         if (ok && tiles > 0) load(before, p.cv, p.nv);
         if (lane == 0) p.info[blockIdx.x] = inf;
         // after a wait that ran out: no copy of this CTA may be in flight when it ends
         if (*abort)
             for (uint32_t i = cnt > NS ? cnt - NS : 0; i < cnt; ++i)
                 mbar_wait_bounded(&ctl.full[i % NS], (i / NS) & 1u, kWaitNs);
-    } else if (warp == kMma) {
-        // ------------------------------------------------------------------ matrix instructions
-        constexpr uint32_t kIdS = mma_desc(FP16, false, kTile, kTile), kIdO = mma_desc(FP16, true, kTile, DP);
+    } else if (warp == kMmaS) {
+        // ------------------------------------------------------------------ S = Q K^T
+        // Tiles are numbered through the part.  S of a tile is issued as soon as its K, its segment's Q and its
+        // slot are there.  (One warp for both products was busy with its own waits for 2300 cycles a tile; the
+        // products alone take 1060.)
+        constexpr uint32_t kId = mma_desc(FP16, false, kTile, kTile);
         const uint32_t id_new = mma_desc(FP16, false, kTile, p.nb);
-        // Tiles are numbered through the part.  S of the next tile is issued before O of this one; the first S
-        // of a segment, which waits for its Q, behind the last O of the one before.
-        bool ok = true;
         const bool one = lane == 0;
         const uint64_t q_desc = mat_desc(smem_addr(sm_q), 16, 1024);
-        const uint32_t n_tiles = static_cast<uint32_t>(ctl.hi - ctl.lo);
-        uint32_t u = 0, naux = 0, seg = 0;
-        auto issue_s = [&](uint32_t w, bool drafted) {
-            const uint32_t cnt = w == 0 ? 0 : 2 * w - 1, st = cnt % NS, slot = w % 3;   // (in the producer's order)
-            if (w >= 3) ok = ok && wait(&ctl.pv_done[slot], w / 3 - 1);
-            ok = ok && wait(&ctl.full[st], cnt / NS);
-            if (!ok) return;
-            tc_fence_after();
-            const uint64_t k_desc = mat_desc(smem_addr(sm_kv + st * Sh::kTileBytes), 16, 1024);
-            const uint32_t id = drafted ? id_new : kIdS;
-#pragma unroll
-            for (int kk = 0; kk < DP / 16; ++kk) {
-                const uint32_t off = ((kk / 4) * kHalfBytes + (kk % 4) * 32) >> 4;   // (of the address fields)
-                mma_ss(one, tmem + slot * kTile, q_desc + off, k_desc + off, id, kk > 0);
-            }
-            mma_commit(one, &ctl.s_full[slot]);
-            mma_commit(one, &ctl.empty[st]);
-            __syncwarp();
-        };
+        uint32_t u = 0, seg = 0;
+        bool ok = true;
         while (ok && wk.next(p, ctl.lens)) {
             ok = wait(&ctl.q_full, seg++);
-            for (int kt = s.tile0 - 1; ok && kt < s.tile1; ++kt) {
-                // (one place for the code: the round at tile0 - 1 only starts the first S)
-                if (kt + 1 < s.tile1) issue_s(u + (kt >= s.tile0 ? 1 : 0), kt + 1 == s.tiles - 1);
-                if (!ok || kt < s.tile0) continue;
-                const uint32_t cnt = u + 1 == n_tiles ? 2 * u + 1 : 2 * u + 2, st = cnt % NS, slot = u % 3;
+            for (int kt = s.tile0; ok && kt < s.tile1; ++kt, ++u) {
+                const uint32_t cnt = u < 2 ? u : 2 * u - 2, st = cnt % NS, slot = u % 3;   // (in the producer's order)
+                if (u >= 3) ok = wait(&ctl.pv_done[slot], u / 3 - 1);
+                ok = ok && wait(&ctl.full[st], cnt / NS);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t k_desc = mat_desc(smem_addr(sm_kv + st * Sh::kTileBytes), 16, 1024);
+                const uint32_t id = kt == s.tiles - 1 ? id_new : kId;
+#pragma unroll
+                for (int kk = 0; kk < DP / 16; ++kk) {
+                    const uint32_t off = ((kk / 4) * kHalfBytes + (kk % 4) * 32) >> 4;   // (of the address fields)
+                    mma_ss(one, tmem + slot * kTile, q_desc + off, k_desc + off, id, kk > 0);
+                }
+                mma_commit(one, &ctl.s_full[slot]);
+                mma_commit(one, &ctl.empty[st]);
+                __syncwarp();
+            }
+        }
+        // nothing may be in flight when TMEM is freed
+        mma_commit(one, &ctl.drain[0]);
+        __syncwarp();
+        mbar_wait_bounded(&ctl.drain[0], 0, kWaitNs);
+    } else if (warp == kMmaO) {
+        // ------------------------------------------------------------------ O += P V
+        constexpr uint32_t kId = mma_desc(FP16, true, kTile, DP);
+        const bool one = lane == 0;
+        const uint32_t n_tiles = static_cast<uint32_t>(ctl.hi - ctl.lo);
+        uint32_t u = 0, naux = 0;
+        bool ok = true;
+        while (ok && wk.next(p, ctl.lens)) {
+            for (int kt = s.tile0; ok && kt < s.tile1; ++kt, ++u) {
+                const uint32_t cnt = u + 2 >= n_tiles ? n_tiles + u : 2 * u + 3, st = cnt % NS, slot = u % 3;
                 uint8_t* v = sm_kv + st * Sh::kTileBytes;
                 const bool drafted = kt == s.tiles - 1;
                 const int valid = drafted ? p.nb : min(kTile, s.len - kt * kTile);
@@ -489,7 +502,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                 tc_fence_after();
                 const uint64_t v_desc = mat_desc(smem_addr(v), kHalfBytes, 1024);
                 auto step = [&](int kk) {
-                    mma_ts(one, tmem + 3 * kTile, tmem + slot * kTile + kk * 8, v_desc + (kk * 2048 >> 4), kIdO,
+                    mma_ts(one, tmem + 3 * kTile, tmem + slot * kTile + kk * 8, v_desc + (kk * 2048 >> 4), kId,
                            kt > s.tile0 || kk > 0);
                 };
                 if (steps == kTile / 16) {
@@ -502,13 +515,11 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                 mma_commit(one, &ctl.pv_done[slot]);
                 mma_commit(one, &ctl.empty[st]);
                 __syncwarp();
-                ++u;
             }
         }
-        // nothing may be in flight when TMEM is freed
-        mma_commit(one, &ctl.drain);
+        mma_commit(one, &ctl.drain[1]);
         __syncwarp();
-        mbar_wait_bounded(&ctl.drain, 0, kWaitNs);
+        mbar_wait_bounded(&ctl.drain[1], 0, kWaitNs);
     } else {
         // ------------------------------------------------------------------ softmax: thread = row
         // warpgroup wg takes the tiles with number % 2 == wg, and half of O's columns at a segment's end
@@ -771,7 +782,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMma) tmem_free(tmem, 512);
+    if (warp == kMmaS) tmem_free(tmem, 512);
 }
 
 // Joins the parts of the item that starts in part blockIdx.x and goes on: one warp per row, the parts
