@@ -136,7 +136,7 @@ struct Walker {
 };
 
 struct Control {
-    uint64_t full[16], empty[16];
+    uint64_t full[2][6], empty[2][6];   // of the K ring, of the V ring
     uint64_t s_full[3], p_full[3], pv_done[3], m_ready[4][2], pair[4], aux[2], q_full, drain[2];
     long long lo, hi, base, total, parts;
     unsigned long long poison[2];  // drafted nodes with a V element that is not finite (alternating)
@@ -222,11 +222,11 @@ template <bool FP16, int DP>
 struct Shape {
     static constexpr int kHalves = DP / 64;
     static constexpr int kTileBytes = kTile * DP * 2;
-    static constexpr int kStages = DP == 128 ? 6 : 12;   // of the ring, a K or a V tile each
-    static constexpr int kSmem = (1 + kStages) * kTileBytes + static_cast<int>(sizeof(Control));
+    static constexpr int kStages = DP == 128 ? 3 : 6;   // of the K ring and of the V ring
+    static constexpr int kSmem = (1 + 2 * kStages) * kTileBytes + static_cast<int>(sizeof(Control));
     static constexpr int kSoftmaxWarps = 8;
-    static constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
-    static_assert(kStages <= 16 && kSmem <= 232448, "shared memory");
+    static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
+    static_assert(kStages <= 6 && kSmem <= 232448, "shared memory");
 };
 
 template <bool FP16, int DP>
@@ -242,18 +242,20 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
     }
     uint8_t* sm_q = dyn;
     uint8_t* sm_kv = dyn + Sh::kTileBytes;
-    Control& ctl = *reinterpret_cast<Control*>(sm_kv + NS * Sh::kTileBytes);
+    Control& ctl = *reinterpret_cast<Control*>(sm_kv + 2 * NS * Sh::kTileBytes);
     const svd_tree_attention_args& a = p.a;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    constexpr int kProducer = Sh::kSoftmaxWarps, kMmaS = Sh::kSoftmaxWarps + 1, kMmaO = Sh::kSoftmaxWarps + 2;
-    volatile int* const abort = &ctl.abort;
+    constexpr int kLoadK = Sh::kSoftmaxWarps, kMmaS = kLoadK + 1, kMmaO = kLoadK + 2, kLoadV = kLoadK + 3;
     const int part = blockIdx.x / p.NR, rg = blockIdx.x % p.NR;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == kMmaS) {
         if (lane == 0) {
-            for (int i = 0; i < NS; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
+            for (int i = 0; i < 2 * NS; ++i) {
+                mbar_init(&ctl.full[i % 2][i / 2], 1);
+                mbar_init(&ctl.empty[i % 2][i / 2], 1);
+            }
             for (int i = 0; i < 3; ++i) {
                 mbar_init(&ctl.s_full[i], 1);
                 mbar_init(&ctl.p_full[i], 4);
@@ -273,7 +275,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
             ctl.abort = 0;
         }
         tmem_alloc(&ctl.tmem, 512);
-    } else if (warp == kProducer) {
+    } else if (warp == kLoadK) {
         if (lane == 0) { prefetch_map(&p.ck); prefetch_map(&p.cv); prefetch_map(&p.nk); prefetch_map(&p.nv); }
     } else if (warp == 0) {
         // this CTA's part of the line of tiles, and the sequence in which it begins
@@ -331,39 +333,16 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         return __all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)) || wait_on(bar, parity & 1u, &ctl.abort, p.status);
     };
 
-    if (warp == kProducer) {
+    if (warp == kLoadK || warp == kLoadV) {
         // ------------------------------------------------------------------ producer
-        // S is formed two tiles ahead of O, so V of a tile follows K of the second next one
-        struct Tile {
-            int page, row, hk, b;       // lane's page and row in it (row < 0: the drafted tile)
-        };
-        uint32_t cnt = 0, tiles = 0;    // loads and tiles so far
-        Tile before = {-1, -1, 0, 0}, before2 = before;
+        // one warp for K, one for V
+        const int kv = warp == kLoadV ? 1 : 0;
+        const CUtensorMap* const cached = kv ? &p.cv : &p.ck;
+        const CUtensorMap* const fresh = kv ? &p.nv : &p.nk;
+        uint64_t* const full = ctl.full[kv];
+        const bool one = lane == 0;
+        uint32_t u = 0;                 // tiles so far
         bool ok = true;
-        auto load = [&](const Tile& g, const CUtensorMap& cached, const CUtensorMap& drafted) {
-            const uint32_t st = cnt % NS;
-            if (cnt >= NS && !wait(&ctl.empty[st], cnt / NS - 1)) return false;
-            ++cnt;
-            uint8_t* dst = sm_kv + st * Sh::kTileBytes;
-            if (g.row >= 0) {
-                const uint32_t box = p.page_rows * 128u;
-                const int boxes = __popc(__ballot_sync(0xffffffffu, g.page >= 0));
-                if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], boxes * kHalves * box);
-                __syncwarp();
-                if (g.page >= 0) {
-#pragma unroll
-                    for (int h = 0; h < kHalves; ++h)
-                        tma_load_4d(dst + h * kHalfBytes + lane * box, &cached, h * 64, g.hk, g.row, g.page, &ctl.full[st]);
-                }
-            } else if (lane == 0) {
-                mbar_arrive_expect_tx(&ctl.full[st], kHalves * p.nb * 128u);
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h)
-                    tma_load_4d(dst + h * kHalfBytes, &drafted, h * 64, g.hk, 0, g.b, &ctl.full[st]);
-            }
-            __syncwarp();
-            return true;
-        };
         PartInfo inf = {0, 0, -1};   // the item that starts here and goes on in later parts
         while (ok && wk.next(p, ctl.lens)) {
             if (s.tile0 == 0 && s.tile1 < s.tiles) {
@@ -387,23 +366,41 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                 return pg;
             };
             int pg = page_of(s.tile0);
-            for (int tile = s.tile0; ok && tile < s.tile1; ++tile) {
+            for (int tile = s.tile0; tile < s.tile1; ++tile, ++u) {
                 const int next_pg = tile + 1 < s.tile1 ? page_of(tile + 1) : -1;
-                const Tile now = {pg, tile < ctiles ? (tile * kTile + lane * p.page_rows) & (a.page_size - 1) : -1, s.hk, s.b};
-                ok = load(now, p.ck, p.nk);
-                if (ok && tiles++ > 1) ok = load(before2, p.cv, p.nv);
-                before2 = before;
-                before = now;
+                const uint32_t st = u % NS;
+                if (u >= NS) ok = wait(&ctl.empty[kv][st], u / NS - 1);
+                if (!ok) break;
+                uint8_t* dst = sm_kv + (kv * NS + st) * Sh::kTileBytes;
+                if (tile < ctiles) {
+                    // box by box in code that the warp runs together: issued lane by lane, the 16 boxes of a tile of
+                    // 16-token pages took 1600 cycles
+                    const uint32_t box = p.page_rows * 128u;
+                    const int boxes = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+                    const int row = (tile * kTile) & (a.page_size - 1);   // (0 unless pages are longer than tiles)
+                    if (one) mbar_arrive_expect_tx(&full[st], boxes * kHalves * box);
+                    __syncwarp();
+#pragma unroll 2
+                    for (int i = 0; i < boxes; ++i) {
+                        const int page = __shfl_sync(0xffffffffu, pg, i);
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h)
+                            tma_load_4d(one, dst + h * kHalfBytes + i * box, cached, h * 64, s.hk, row, page, &full[st]);
+                    }
+                } else {
+                    if (one) mbar_arrive_expect_tx(&full[st], kHalves * p.nb * 128u);
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) tma_load_4d(one, dst + h * kHalfBytes, fresh, h * 64, s.hk, 0, s.b, &full[st]);
+                }
+                __syncwarp();
                 pg = next_pg;
             }
         }
-        if (ok && tiles > 1) ok = load(before2, p.cv, p.nv);
-        if (ok && tiles > 0) load(before, p.cv, p.nv);
-        if (lane == 0) p.info[blockIdx.x] = inf;
+        if (one && kv == 0) p.info[blockIdx.x] = inf;
         // after a wait that ran out: no copy of this CTA may be in flight when it ends
-        if (*abort)
-            for (uint32_t i = cnt > NS ? cnt - NS : 0; i < cnt; ++i)
-                mbar_wait_bounded(&ctl.full[i % NS], (i / NS) & 1u, kWaitNs);
+        if (!ok)
+            for (uint32_t i = u > NS ? u - NS : 0; i < u; ++i) mbar_wait_bounded(&full[i % NS], (i / NS) & 1u, kWaitNs);
     } else if (warp == kMmaS) {
         // ------------------------------------------------------------------ S = Q K^T
         // Tiles are numbered through the part.  S of a tile is issued as soon as its K, its segment's Q and its
@@ -418,9 +415,9 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         while (ok && wk.next(p, ctl.lens)) {
             ok = wait(&ctl.q_full, seg++);
             for (int kt = s.tile0; ok && kt < s.tile1; ++kt, ++u) {
-                const uint32_t cnt = u < 2 ? u : 2 * u - 2, st = cnt % NS, slot = u % 3;   // (in the producer's order)
+                const uint32_t st = u % NS, slot = u % 3;
                 if (u >= 3) ok = wait(&ctl.pv_done[slot], u / 3 - 1);
-                ok = ok && wait(&ctl.full[st], cnt / NS);
+                ok = ok && wait(&ctl.full[0][st], u / NS);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t k_desc = mat_desc(smem_addr(sm_kv + st * Sh::kTileBytes), 16, 1024);
@@ -431,7 +428,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                     mma_ss(one, tmem + slot * kTile, q_desc + off, k_desc + off, id, kk > 0);
                 }
                 mma_commit(one, &ctl.s_full[slot]);
-                mma_commit(one, &ctl.empty[st]);
+                mma_commit(one, &ctl.empty[0][st]);
                 __syncwarp();
             }
         }
@@ -443,17 +440,16 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         // ------------------------------------------------------------------ O += P V
         constexpr uint32_t kId = mma_desc(FP16, true, kTile, DP);
         const bool one = lane == 0;
-        const uint32_t n_tiles = static_cast<uint32_t>(ctl.hi - ctl.lo);
         uint32_t u = 0, naux = 0;
         bool ok = true;
         while (ok && wk.next(p, ctl.lens)) {
             for (int kt = s.tile0; ok && kt < s.tile1; ++kt, ++u) {
-                const uint32_t cnt = u + 2 >= n_tiles ? n_tiles + u : 2 * u + 3, st = cnt % NS, slot = u % 3;
-                uint8_t* v = sm_kv + st * Sh::kTileBytes;
+                const uint32_t st = u % NS, slot = u % 3;
+                uint8_t* v = sm_kv + (NS + st) * Sh::kTileBytes;
                 const bool drafted = kt == s.tiles - 1;
                 const int valid = drafted ? p.nb : min(kTile, s.len - kt * kTile);
                 const int steps = (valid + 15) >> 4;
-                ok = wait(&ctl.full[st], cnt / NS);
+                ok = wait(&ctl.full[1][st], u / NS);
                 if (!ok) break;
                 if (drafted) {
                     // rows of padding nodes become zero; elements that are not finite are taken out
@@ -513,7 +509,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                     for (int kk = 0; kk < steps; ++kk) step(kk);
                 }
                 mma_commit(one, &ctl.pv_done[slot]);
-                mma_commit(one, &ctl.empty[st]);
+                mma_commit(one, &ctl.empty[1][st]);
                 __syncwarp();
             }
         }
@@ -870,8 +866,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
     tree_attention_kernel<FP16, DP><<<ctas, Sh::kThreads, Sh::kSmem, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof cfg);
+    cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
