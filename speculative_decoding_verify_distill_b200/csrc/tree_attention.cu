@@ -450,6 +450,8 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                 const int valid = drafted ? p.nb : min(kTile, s.len - kt * kTile);
                 const int steps = (valid + 15) >> 4;
                 ok = wait(&ctl.full[1][st], u / NS);
+                // (S of a drafted tile: every warp has left the segment before last, whose note is replaced here)
+                if (drafted) ok = ok && wait(&ctl.s_full[slot], u / 3);
                 if (!ok) break;
                 if (drafted) {
                     // rows of padding nodes become zero; elements that are not finite are taken out
