@@ -639,6 +639,11 @@ def _pages(t, name: str, dtype, like, dev):
     return ctypes.c_void_p(t.data_ptr()), stride
 
 
+def _raw_stream(index: int) -> int:
+    """cudaStream_t of the current stream of a device."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 class _TreeOp:
     """Preallocated outputs, argument block and workspace of one operator, for repeated calls.
 
@@ -653,9 +658,10 @@ class _TreeOp:
         with torch.cuda.device(dev):
             self.ws = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
             self._last = torch.cuda.current_stream(dev)
+        self._raw = self._last.cuda_stream
         assert self.ws.data_ptr() % 256 == 0
         self._call = getattr(lib(), self._fn)
-        self._ws = (ctypes.c_void_p(self.ws.data_ptr()), self.ws.numel())
+        self._ws, self._nws = ctypes.c_void_p(self.ws.data_ptr()), self.ws.numel()
         self._ref = ctypes.byref(args)
 
     def _order(self, s):
@@ -667,24 +673,27 @@ class _TreeOp:
             s.wait_stream(self._last)
             for t in [self.ws, *self.outputs().values()]:
                 t.record_stream(s)
-            self._last = s
+            self._last, self._raw = s, s.cuda_stream
 
     def __call__(self, stream=None):
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        if s.cuda_stream != self._last.cuda_stream or s.device != self.device:
-            self._order(s)
+        # the raw handle is enough while the stream stays the same (a Stream object costs 2 us)
+        raw = _raw_stream(self.device.index) if stream is None else stream.cuda_stream
+        if raw != self._raw or stream is not None and stream.device != self.device:
+            self._order(torch.cuda.current_stream(self.device) if stream is None else stream)
         if torch.cuda.current_device() == self.device.index:
-            _check(self._call(self._ref, *self._ws, s.cuda_stream), self._fn)
+            code = self._call(self._ref, self._ws, self._nws, raw)
         else:
             with torch.cuda.device(self.device):
-                _check(self._call(self._ref, *self._ws, s.cuda_stream), self._fn)
+                code = self._call(self._ref, self._ws, self._nws, raw)
+        if code:
+            raise SvdError(code, self._fn)
         return self
 
     def device_error(self, stream=None) -> int:
         """The status word of the calls so far (synchronizes)."""
         with torch.cuda.device(self.device):
             s = self._last if stream is None else stream
-            return int(lib().svd_get_device_error(self._ws[0], s.cuda_stream))
+            return int(lib().svd_get_device_error(self._ws, s.cuda_stream))
 
 
 def _once(op, args, kw, stream):
