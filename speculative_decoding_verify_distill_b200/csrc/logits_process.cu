@@ -7,13 +7,14 @@
 // sequence and all of its rows (or a group of them).  Once, it builds a table of its chunk in shared
 // memory (one word per id: prompt flag, count in the generated history, index of the drafted nodes
 // with this token, bias) and the list of the ids that the table has anything for ("touched").  Rows then
-// stream through a two-stage ring of bulk copies, two rows a stage: all threads share the (row, touched
-// id) pairs of a stage and change those elements in shared memory, and behind one barrier every
-// thread takes whole vectors: mask, store, maximum.
+// stream through a two-stage ring of bulk copies, two rows a stage.  A warp owns 512 of the ids in every row (every
+// eighth block of 64: touched ids crowd among the low ones) and works without the others: its lanes share the (row, touched id) pairs of a stage and change those
+// elements in shared memory, and then every lane takes whole vectors: mask, store, maximum.
 //
 // The pairs are what makes the touched ids cheap.  They are few and anywhere, so nearly every warp's
 // vectors hold one; worked on by the lane that holds its vector, they cost every warp the arithmetic
-// for one or two lanes (130 us at 32 x 17 rows of 151936 with 1536 tokens of history, 84 with the pairs).
+// for one or two lanes (130 us at 32 x 17 rows of 151936 with 1536 tokens of history).  Sharing them over the
+// whole CTA took a barrier a stage (84 us); over a warp it takes none (79 us).
 //
 // Ancestors' tokens differ from row to row.  They need no per-row table: the table names, for an
 // id that some node drafted, the set of nodes with that token (64 bits), and the row's count is
@@ -23,6 +24,7 @@
 // rounded values (and the argmax taken over them) are fixed bit for bit.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -32,12 +34,13 @@ namespace svd {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kVecs = 2;                       // vectors of 8 ids per thread and row
-constexpr int kChunk = 8 * kVecs * kThreads;   // ids per CTA
+constexpr int kWarps = 8;                      // that work on rows; one more fills the stages
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kVecs = 2;                       // vectors of 8 ids per lane and row
+constexpr int kWarpIds = 8 * 32 * kVecs;       // ids of a warp
+constexpr int kChunk = kWarps * kWarpIds;      // ids per CTA
 constexpr int kStages = 2;
-constexpr int kAhead = 4;                      // pairs per thread whose raw logits the gradient loads ahead
+constexpr int kAhead = 4;                      // pairs per lane whose raw logits the gradient loads ahead
 constexpr int kStageBytes = 4 * kChunk;        // two rows of bf16 or one of fp32
 constexpr int kFewCtas = 444;                  // three per SM
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -54,8 +57,9 @@ struct Tables {
     unsigned long long nodes[kTreeMaxNodes];   // nodes that share the token of their lowest one
     uint4 best[kWarps][kTreeMaxNodes];         // each warp's best vector of each row,
     int best_at[kWarps][kTreeMaxNodes];        // and its first id (-1: none)
-    uint64_t full[kStages];
-    int scan[kWarps];
+    uint64_t full[kStages], empty[kStages];
+    int scan[kWarps + 1];
+    int start[kWarps + 1];                     // of each warp's part of the list
     int tok[kTreeMaxNodes];
     int8_t parent[kTreeMaxNodes];
     int last, repeated;
@@ -65,7 +69,7 @@ struct Dyn {                                   // dynamic shared memory
     uint8_t* stage;                            // [kStages][kStageBytes]
     uint32_t* tab;                             // [kChunk]
     uint32_t* touched;                         // [kChunk / 32]
-    uint16_t* list;                            // [kChunk]: touched ids, ascending
+    uint16_t* list;                            // [kChunk]: touched ids, by owning warp
     uint32_t* bias_word;                       // [n_bias]
     float* bias;                               // [n_bias]
 };
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 3) logits_process_kernel(LogitsParam
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ Tables s;
     const svd_logits_process_args& a = p.a;
-    const int t = threadIdx.x, lane = t & 31, b = blockIdx.x, V = a.V;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, b = blockIdx.x, V = a.V;
     const int v0 = blockIdx.y * kChunk, v1 = min(V, v0 + kChunk);
     const int j0 = blockIdx.z * p.rows_per_cta, j1 = min(a.n, j0 + p.rows_per_cta);
     const int n_bias = GRAD ? 0 : a.n_bias;
@@ -217,32 +221,30 @@ __global__ void __launch_bounds__(kThreads, 3) logits_process_kernel(LogitsParam
     const bool sparse = src == dst && !want_arg && !a.mask;
     const int batches = sparse ? 0 : (j1 - j0 + kRows - 1) / kRows;
 
-    // rows of batch k into its stage
+    // (one thread) rows of batch k into its stage
     auto fetch = [&](int k) {
         uint8_t* to = d.stage + (k % kStages) * kStageBytes;
         const int j = j0 + k * kRows, rows = min(kRows, j1 - j);
-        if (ALIGNED) {
-            if (t != 0) return;
-            const uint32_t bytes = static_cast<uint32_t>(v1 - v0) * sizeof(T);
-            mbar_arrive_expect_tx(&s.full[k % kStages], rows * bytes);
-            for (int r = 0; r < rows; ++r)
-                bulk_load(to + r * kChunk * sizeof(T), src + static_cast<size_t>(j + r) * V + v0, bytes, &s.full[k % kStages]);
-        } else {
-            for (int r = 0; r < rows; ++r)
-                for (int i = t; i < v1 - v0; i += kThreads)
-                    reinterpret_cast<T*>(to)[r * kChunk + i] = src[static_cast<size_t>(j + r) * V + v0 + i];
-        }
+        const uint32_t bytes = static_cast<uint32_t>(v1 - v0) * sizeof(T);
+        mbar_arrive_expect_tx(&s.full[k % kStages], rows * bytes);
+        for (int r = 0; r < rows; ++r)
+            bulk_load(to + r * kChunk * sizeof(T), src + static_cast<size_t>(j + r) * V + v0, bytes, &s.full[k % kStages]);
     };
-    if (ALIGNED && t == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1);
+    if (ALIGNED && warp == kWarps && lane == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], kWarps);
+        }
         fence_mbar_init();
+        // the first rows arrive while the table is built
+        for (int k = 0; k < kStages && k < batches; ++k) fetch(k);
     }
-    // the first rows arrive while the table is built
-    for (int k = 0; k < kStages && k < batches; ++k) fetch(k);
     build_tables(p, b, v0, v1, n_bias, s, d);
 
-    // the list of touched ids
-    const uint32_t tw = t < kChunk / 32 ? d.touched[t] : 0u;
+    // the list of touched ids, warp by warp
+    // thread t: word t % 16 of the ids of warp t / 16, so that each warp's part of the list is contiguous
+    const int word = (((t & 15) >> 1) * kWarps + (t >> 4)) * 2 + (t & 1);
+    const uint32_t tw = t < kChunk / 32 ? d.touched[word] : 0u;
     int n_touched;
     {
         const int mine = __popc(tw);
@@ -252,16 +254,18 @@ __global__ void __launch_bounds__(kThreads, 3) logits_process_kernel(LogitsParam
             const int y = __shfl_up_sync(0xffffffffu, rank, o);
             if (lane >= o) rank += y;
         }
-        if (lane == 31) s.scan[t >> 5] = rank;
+        if (lane == 31) s.scan[warp] = rank;
         __syncthreads();
         n_touched = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < (t >> 5)) rank += s.scan[w];
+        for (int w = 0; w <= kWarps; ++w) {
+            if (w < warp) rank += s.scan[w];
             n_touched += s.scan[w];
         }
         rank -= mine;
-        for (uint32_t bits = tw; bits; bits &= bits - 1) d.list[rank++] = static_cast<uint16_t>(t * 32 + __ffs(bits) - 1);
+        if (t < kChunk / 32 && t % (kWarpIds / 32) == 0) s.start[t / (kWarpIds / 32)] = rank;
+        if (t == 0) s.start[kWarps] = n_touched;
+        for (uint32_t bits = tw; bits; bits &= bits - 1) d.list[rank++] = static_cast<uint16_t>(word * 32 + __ffs(bits) - 1);
     }
     __syncthreads();
 
@@ -304,8 +308,21 @@ __global__ void __launch_bounds__(kThreads, 3) logits_process_kernel(LogitsParam
     const uint8_t* const mask = reinterpret_cast<const uint8_t*>(a.mask) + (row_mask ? row0 : static_cast<size_t>(b)) * W4;
     const uint32_t mval = __bfloat16_as_ushort(__float2bfloat16_rn(GRAD ? 0.f : a.mask_value));
     const uint32_t fill = mval | mval << 16;
-    const int pairs = n_touched * kRows;
-    // mask bytes of a batch, and the gradient's raw logits of this thread's first pairs, go out a batch ahead
+    bool ok = true;
+    if (warp == kWarps) {
+        // refills a stage when every warp has left it
+        for (int k = kStages; ALIGNED && ok && k < batches; ++k) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s.empty[k % kStages], (k / kStages - 1) & 1, kWaitNs)) != 0;
+            if (ok && lane == 0) fetch(k);
+            __syncwarp();
+        }
+    }
+    const int mine = warp < kWarps ? batches : 0;
+    // the lane's vectors: eight lanes take a block of 64 ids
+    auto id8 = [&](int q) { return ((q * 4 + (lane >> 3)) * kWarps + warp) * 64 + (lane & 7) * 8; };
+    const uint16_t* const list = d.list + (warp < kWarps ? s.start[warp] : 0);
+    const int pairs = warp < kWarps ? (s.start[warp + 1] - s.start[warp]) * kRows : 0;
+    // mask bytes of a batch, and the gradient's raw logits of this lane's first pairs, go out a batch ahead
     uint32_t ms[kRows][kVecs];
     uint16_t raws[kAhead] = {};
     auto prefetch = [&](int k) {
@@ -314,43 +331,62 @@ __global__ void __launch_bounds__(kThreads, 3) logits_process_kernel(LogitsParam
             const int j = j0 + k * kRows + r;
 #pragma unroll
             for (int q = 0; q < kVecs; ++q) {
-                const int v = v0 + (q * kThreads + t) * 8;
+                const int v = v0 + id8(q);
                 if (a.mask && j < j1 && v < v1) ms[r][q] = __ldg(mask + (row_mask ? j * W4 : 0) + (v >> 3));
             }
         }
 #pragma unroll
         for (int u = 0; GRAD && u < kAhead; ++u) {
-            const int i = t + u * kThreads, j = j0 + k * kRows + i % kRows;
-            if (i < pairs && j < j1) raws[u] = __ldg(raw + static_cast<size_t>(j) * V + v0 + d.list[i / kRows]);
+            const int i = lane + u * 32, j = j0 + k * kRows + i % kRows;
+            if (i < pairs && j < j1) raws[u] = __ldg(raw + static_cast<size_t>(j) * V + v0 + list[i / kRows]);
         }
     };
-    prefetch(0);
+    if (mine) prefetch(0);
 
-    bool ok = true;
-    for (int k = 0; k < batches; ++k) {
+    for (int k = 0; k < mine; ++k) {
         T* const st = reinterpret_cast<T*>(d.stage + (k % kStages) * kStageBytes);
         const int jb = j0 + k * kRows;
-        if (ALIGNED) ok = mbar_wait_bounded(&s.full[k % kStages], (k / kStages) & 1, kWaitNs);
-        else __syncthreads();   // the stage was filled by all threads
-        auto pair = [&](int i, uint16_t raw_logit) {
-            const int r = i % kRows, at = d.list[i / kRows];
-            const float x = as_f32(st[r * kChunk + at]);
-            st[r * kChunk + at] = as_t(changed(x, GRAD ? f32(raw_logit) > 0.f : x > 0.f, at, jb + r));
-        };
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int i = t + u * kThreads;
-            if (i < pairs && jb + i % kRows < j1) pair(i, raws[u]);
+        if (ALIGNED) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s.full[k % kStages], (k / kStages) & 1, kWaitNs)) != 0;
+            if (!ok) break;
+        } else {
+            // each warp brings its own ids
+            for (int r = 0; r < kRows && jb + r < j1; ++r)
+                for (int i = lane; i < kWarpIds; i += 32) {
+                    const int at = ((i >> 6) * kWarps + warp) * 64 + (i & 63);
+                    if (v0 + at < v1) st[r * kChunk + at] = src[static_cast<size_t>(jb + r) * V + v0 + at];
+                }
+            __syncwarp();
         }
-        for (int i = t + kAhead * kThreads; i < pairs; i += kThreads)
-            if (jb + i % kRows < j1)
-                pair(i, GRAD ? __ldg(raw + static_cast<size_t>(jb + i % kRows) * V + v0 + d.list[i / kRows]) : uint16_t(0));
-        // One barrier a batch: the pairs are done, and every thread has left the batch before, whose
-        // stage is filled anew.
-        if (ALIGNED) fence_async();
-        ok = __syncthreads_and(ok);
-        if (!ok) break;
-        if (k > 0 && k - 1 + kStages < batches) fetch(k - 1 + kStages);
+        // new value of pair i; behind the last one, any value
+        auto value = [&](int i, uint16_t raw_logit) {
+            const int c = min(i, pairs - 1), r = c % kRows, at = list[c / kRows];
+            const float x = as_f32(st[r * kChunk + at]);
+            return changed(x, GRAD ? f32(raw_logit) > 0.f : x > 0.f, at, min(jb + r, a.n - 1));
+        };
+        auto put = [&](int i, float x) {
+            if (i < pairs && jb + i % kRows < j1) st[i % kRows * kChunk + list[i / kRows]] = as_t(x);
+        };
+        if (pairs <= 32) {
+            if (pairs > 0) put(lane, value(lane, raws[0]));
+        } else {
+            // several at once: one alone waits through shared memory, the division and (behind the first
+            // kAhead) the raw logit
+#pragma unroll 1
+            for (int i = lane; i - lane < pairs; i += 32 * kAhead) {
+                float x[kAhead];
+#pragma unroll
+                for (int u = 0; GRAD && u < kAhead; ++u) {
+                    const int c = min(i + u * 32, pairs - 1);
+                    if (i != lane) raws[u] = __ldg(raw + static_cast<size_t>(min(jb + c % kRows, a.n - 1)) * V + v0 + list[c / kRows]);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) x[u] = value(i + u * 32, raws[u]);
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) put(i + u * 32, x[u]);
+            }
+        }
+        __syncwarp();
         uint32_t mk[kRows][kVecs];
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
@@ -366,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 3) logits_process_kernel(LogitsParam
             int best_at = -1;
 #pragma unroll
             for (int q = 0; q < kVecs; ++q) {
-                const int i8 = (q * kThreads + t) * 8, v = v0 + i8;
+                const int i8 = id8(q), v = v0 + i8;
                 if (v >= v1) continue;
                 const size_t off = static_cast<size_t>(j) * V + v;
                 if (F32) {
@@ -419,14 +455,22 @@ __global__ void __launch_bounds__(kThreads, 3) logits_process_kernel(LogitsParam
                 const bool num = best_m == best_m;
                 const float top = redux_max_f32(num ? best_m : -INFINITY);
                 const unsigned win = __ballot_sync(0xffffffffu, num && best_m == top);
-                const unsigned low = __ballot_sync(0xffffffffu, num && best_m == top && best_at == v0 + t * 8);
+                const unsigned low = __ballot_sync(0xffffffffu, num && best_m == top && best_at == v0 + id8(0));
                 if (lane == (win ? __ffs(low ? low : win) - 1 : 0)) {
-                    s.best[t >> 5][j - j0] = best;
-                    s.best_at[t >> 5][j - j0] = win ? best_at : -1;
+                    s.best[warp][j - j0] = best;
+                    s.best_at[warp][j - j0] = win ? best_at : -1;
                 }
             }
         }
+        if (ALIGNED) {
+            fence_async();      // the stage is written by copies again
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.empty[k % kStages]);
+        } else {
+            __syncwarp();
+        }
     }
+    ok = __syncthreads_and(ok) != 0;
     if (!ok) {   // a copy did not arrive in time: record it, and leave no copy in flight
         if (t == 0) {
             set_device_error(p.status, SVD_ERR_TIMEOUT);
@@ -437,7 +481,6 @@ __global__ void __launch_bounds__(kThreads, 3) logits_process_kernel(LogitsParam
     if (!want_arg) return;
     // one atomic maximum per row and CTA (a maximum does not depend on the order); the last CTA of
     // the sequence turns the keys into ids and leaves the workspace zero
-    __syncthreads();
     if (t < j1 - j0) {
         unsigned long long key = 0;
         for (int w = 0; w < kWarps; ++w) {
@@ -465,10 +508,11 @@ template <bool GRAD, bool F32, bool ALIGNED>
 cudaError_t launch(const LogitsParams& in, cudaStream_t st) {
     LogitsParams p = in;
     const int chunks = (p.a.V + kChunk - 1) / kChunk;
-    // rows are split over CTAs only where the chunks alone leave SMs without work: every split builds
-    // the chunk's table again
-    int splits = kFewCtas / (chunks * p.a.B);
-    splits = splits < 1 ? 1 : (splits > p.a.n ? p.a.n : splits);
+    // Every split of the rows builds the chunk's table again.  They are split so far that no SM is without
+    // work, and into groups of eight or more to give two rounds of CTAs, behind which a chunk with many touched ids
+    // does not stand alone (8 x 64 rows of 151936: 100 us with one round, 82 us with two).
+    const int ctas = chunks * p.a.B, fill = kFewCtas / ctas, rounds = std::min((2 * kFewCtas + ctas - 1) / ctas, p.a.n / 8);
+    int splits = std::min(p.a.n, std::max(1, std::max(fill, rounds)));
     p.rows_per_cta = (p.a.n + splits - 1) / splits;
     // low ids, which have the most touched ones, start first and do not end up in the tail
     const dim3 grid(p.a.B, chunks, (p.a.n + p.rows_per_cta - 1) / p.rows_per_cta);

@@ -24,6 +24,9 @@ __device__ __forceinline__ int checked_parent(const int32_t* parent, size_t row,
     return -1;
 }
 
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 // Generic-proxy accesses to shared memory before this are ordered before the async proxy's after it.
 __device__ __forceinline__ void fence_async() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
