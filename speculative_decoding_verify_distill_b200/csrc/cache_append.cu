@@ -10,7 +10,7 @@ namespace svd {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kEntries = kThreads / 32;   // per CTA
 
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(AppendParams p) {
@@ -44,10 +44,21 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(AppendParams p) 
             const uint4* vs = static_cast<const uint4*>(a.v_new) + src;
             uint4* kd = static_cast<uint4*>(a.cache_k) + static_cast<size_t>(page) * (a.page_stride_k / 8) + in_page;
             uint4* vd = static_cast<uint4*>(a.cache_v) + static_cast<size_t>(page) * (a.page_stride_v / 8) + in_page;
-            for (int c = lane; c < vecs; c += 32) {
-                const uint4 x = __ldg(ks + c), y = __ldg(vs + c);
-                kd[c] = x;
-                vd[c] = y;
+            // eight loads in flight before the first store (the stores could alias, so the compiler keeps order)
+            for (int c0 = lane; c0 < vecs; c0 += 128) {
+                uint4 x[4], y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c0 + 32 * i < vecs) {
+                        x[i] = __ldcs(ks + c0 + 32 * i);
+                        y[i] = __ldcs(vs + c0 + 32 * i);
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c0 + 32 * i < vecs) {
+                        kd[c0 + 32 * i] = x[i];
+                        vd[c0 + 32 * i] = y[i];
+                    }
             }
         }
     }

@@ -7,8 +7,8 @@
 // arithmetic behind it; with more rows the softmax bounds it (16 exponentials a clock and SM).
 //
 // Work.  An item is one sequence and key head; its keys are tiles of 128: the cached ones, then one tile of
-// the drafted nodes.  All tiles of all items form one line that is cut into equal parts, so ragged
-// lengths balance by themselves and one long sequence spreads over the whole GPU.  A CTA takes one part for
+// the drafted nodes.  All tiles of all items form one line (with a few places for the start and end of each
+// item) that is cut into equal parts, so ragged lengths balance by themselves and one long sequence spreads over the whole GPU.  A CTA takes one part for
 // one group of 128 query rows (a row is a node and a query head); the CTAs of the same part and different
 // groups run side by side and share the part's keys through L2.  A part that holds a whole item writes its
 // result; otherwise it leaves the unnormalised sum with the row maxima and sums in the workspace, and a
@@ -47,6 +47,10 @@ namespace {
 constexpr int kCtas = 148;         // one per SM of a B200
 constexpr int kTile = 128;         // keys per tile, rows per group
 constexpr uint64_t kWaitNs = 1000000000ull;
+// Places of an item on the line besides its tiles: what its start and end cost, in tiles.  With none the parts of
+// many short items ended last: B = 32 of 1 to 4096 tokens took 94 us instead of 77, B = 128 of 500 to 6000 320
+// instead of 294 (four and six places are no better).
+constexpr int kItemCost = 3;
 constexpr int kCombineWarps = 8;
 constexpr int kLens = 64;          // sequences of a part whose lengths are kept in shared memory
 
@@ -99,24 +103,28 @@ struct Segment {
     int b, hk, len;
     int tile0, tile1, tiles;
 };
-// Steps through the segments of the part [lo, hi) of the line of tiles; `base` is where sequence b begins.
+// Steps through the segments of the part [lo, hi) of the line; `base` is where sequence b begins.  On the
+// line an item is kItemCost places, which stand for its start and end, and then its tiles.
 struct Walker {
-    long long pos, hi;
+    long long start, hi;           // where the item begins, and the part ends
     int first;                     // sequence in which the part begins
+    bool any;
     Segment s;
-    __device__ Walker(const AttnParams& p, long long lo, long long end, long long base, int b) : pos(lo), hi(end), first(b) {
-        if (pos >= hi) return;
+    __device__ Walker(const AttnParams& p, long long lo, long long end, long long base, int b) : hi(end), first(b), any(lo < end) {
+        if (!any) return;
         s.b = b;
         s.len = cache_len_of(p, b);
         s.tiles = tiles_of(s.len);
-        const long long r = pos - base;
-        const int it = static_cast<int>(r / s.tiles);
-        s.hk = it;
-        s.tile0 = s.tile1 = static_cast<int>(r - static_cast<long long>(it) * s.tiles);
+        const int width = s.tiles + kItemCost;
+        s.hk = static_cast<int>((lo - base) / width);
+        start = base + static_cast<long long>(s.hk) * width;
+        s.tile0 = s.tile1 = max(0, static_cast<int>(lo - start) - kItemCost);
     }
     __device__ __forceinline__ bool next(const AttnParams& p, const int* lens) {
-        if (pos >= hi) return false;
+        if (!any) return false;
         if (s.tile1 == s.tiles) {      // the item before is done
+            start += s.tiles + kItemCost;
+            if (start >= hi) return any = false;
             s.tile1 = 0;
             if (++s.hk == p.a.Hkv) {
                 s.hk = 0;
@@ -128,10 +136,9 @@ struct Walker {
             }
         }
         s.tile0 = s.tile1;
-        const long long left = hi - pos;
-        s.tile1 = s.tiles - s.tile0 <= left ? s.tiles : s.tile0 + static_cast<int>(left);
-        pos += s.tile1 - s.tile0;
-        return true;
+        const long long left = hi - start - kItemCost;
+        s.tile1 = s.tiles <= left ? s.tiles : max(0, static_cast<int>(left));
+        return any = s.tile1 > s.tile0;
     }
 };
 
@@ -283,7 +290,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         long long total = 0;
         bool bad = false;
         for (int b = lane; b < a.B; b += 32) {
-            total += tiles_of(cache_len_of(p, b));
+            total += tiles_of(cache_len_of(p, b)) + kItemCost;
             if (blockIdx.x == 0 && a.n_pages > 0) bad = bad || __ldg(a.cache_len + b) != cache_len_of(p, b);
             if (blockIdx.x == 0 && a.n_pages == 0) bad = bad || __ldg(a.cache_len + b) != 0;
         }
@@ -297,7 +304,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         int b0 = 0;
         for (int bb = 0; bb < a.B; bb += 32) {
             const int b = bb + lane;
-            long long w = b < a.B ? tiles_of(cache_len_of(p, b)) * HR : 0, x = w;
+            long long w = b < a.B ? (tiles_of(cache_len_of(p, b)) + kItemCost) * HR : 0, x = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -346,7 +353,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         PartInfo inf = {0, 0, -1};   // the item that starts here and goes on in later parts
         while (ok && wk.next(p, ctl.lens)) {
             if (s.tile0 == 0 && s.tile1 < s.tiles) {
-                const long long end = wk.pos + (s.tiles - s.tile1);   // first tile behind the item
+                const long long end = wk.start + kItemCost + s.tiles;   // behind the item
                 long long c = (end - 1) * ctl.parts / ctl.total;
                 while ((c + 1) * ctl.total / ctl.parts < end) ++c;
                 while (c * ctl.total / ctl.parts >= end) --c;

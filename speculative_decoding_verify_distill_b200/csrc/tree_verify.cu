@@ -15,9 +15,9 @@ namespace svd {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kVec = 4;                      // vectors of 8 ids per thread and row
+constexpr int kVec = 8;                      // vectors of 8 ids per thread and row
 constexpr int kChunk = 8 * kThreads * kVec;
 
 struct WalkSmem {

@@ -178,6 +178,23 @@ def test_attention_many_sequences_and_long_one():
     check_attention(attention_case(lens, 1, 4, 1, 128, 64, seed=13))
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,D,dtype", [(3, 8, 8, 128, BF), (40, 4, 2, 64, FP)])
+def test_attention_items_of_one_tile(n, Hq, Hkv, D, dtype):
+    """Many sequences with nothing in the cache, or next to nothing: every part holds many items."""
+    lens = [0] * 300 + [1, 0, 128, 0, 5] * 30
+    c = attention_case(lens, n, Hq, Hkv, D, 16, dtype, seed=18, extra_pages=0)
+    op = check_attention(c, n_nodes=torch.arange(len(lens), device="cuda").remainder(n + 1).to(I32))
+    first = {k: v.clone() for k, v in op.outputs().items()}
+    for _ in range(20):
+        op()
+    assert all(torch.equal(v, first[k]) for k, v in op.outputs().items())
+
+
+def test_attention_more_row_groups_than_sms():
+    """One key head for 1024 query heads of 20 nodes: 160 groups of 128 rows."""
+    check_attention(attention_case([300, 7], 20, 1024, 1, 64, 32, seed=19))
+
+
 def test_attention_no_cache_at_all():
     c = attention_case([0, 0], 6, 4, 2, 64, 16, seed=14)
     empty = torch.empty((0, 16, 2, 64), dtype=BF, device="cuda")
