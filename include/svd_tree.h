@@ -25,6 +25,7 @@
  *     clamped, and page ids outside [0, n_pages) are read as page 0 (attention) or skipped
  *     (append); both record SVD_ERR_PAGE_RANGE.
  *   - Rows of a page behind cache_len are never used, whatever they hold.
+ *   - max_pages * page_size <= 2^30.
  *
  * Conventions as in svd.h: device pointers, row-major and contiguous unless a stride is given,
  * every call enqueues on `stream` and never synchronizes, argument errors are returned before any
@@ -101,7 +102,8 @@ svd_status svd_tree_attention(const svd_tree_attention_args* args, void* ws, siz
  * The gradient with respect to the raw logits, with the counts and the mask of the same lists:
  *   dlogits = masked ? 0 : seen ? (x > 0 ? dz / repetition : dz * repetition) : dz
  * dlogits may be dz itself.
- * Limits: 1 <= n <= 64, 1 <= V <= 327680, hist_stride < 2^23, n_bias <= 4096, n_bias ids of one
+ * Lengths outside [0, hist_stride], and a prompt longer than the history, are clamped.
+ * Limits: B <= 65535, 1 <= n <= 64, 1 <= V <= 327680, hist_stride < 2^23, n_bias <= 4096, n_bias ids of one
  * sequence may repeat (their values add in list order).  V % 8 == 0 with 16-byte aligned logits,
  * out, dz and dlogits takes the fast path.
  * --------------------------------------------------------------------------------------------- */
@@ -151,6 +153,7 @@ svd_status svd_logits_process_grad(const svd_logits_process_args* args, void* ws
  * path and emitted are padded with -1.  Sequences with n_nodes[b] = 0 have an empty path.  On a
  * chain the result is that of svd_verify with b_k = k, kt = k + 1.  node_tok ids outside [0, V) other
  * than -1 match nothing and, where T is given, record SVD_ERR_TOKEN_RANGE; node 0's is not read.
+ * Limits: B <= 65535, 1 <= n <= 64, 1 <= V <= 327680.  Sampled acceptance is the caller's: draw target_tok.
  * --------------------------------------------------------------------------------------------- */
 typedef struct svd_tree_verify_args {
     const uint16_t* T;          /* [B, n, V] bf16, or NULL with target_tok                     */
@@ -179,7 +182,7 @@ svd_status svd_tree_verify(const svd_tree_verify_args* args, void* ws, size_t ws
  * cache_len itself.  The elements are 16 bits wide and are copied as they are.  Entries whose node,
  * page or position is out of range are skipped and recorded (SVD_ERR_TREE, SVD_ERR_PAGE_RANGE).
  * No slot may be named twice by one call (pages shared by sequences end in front of cache_len).
- * Limits: n >= 1, page_size >= 1, Hkv * D % 8 == 0; pointers 16-byte aligned, page strides multiples
+ * Limits: B <= 65535, n >= 1, page_size >= 1, Hkv * D % 8 == 0; pointers 16-byte aligned, page strides multiples
  * of 8 elements.
  * --------------------------------------------------------------------------------------------- */
 typedef struct svd_cache_append_args {

@@ -671,8 +671,9 @@ class _TreeOp:
             capturing = torch.cuda.is_current_stream_capturing()
         if not capturing:
             s.wait_stream(self._last)
-            for t in [self.ws, *self.outputs().values()]:
-                t.record_stream(s)
+            for t in [self.ws, *self._keep, *self.outputs().values()]:
+                if t is not None:
+                    t.record_stream(s)
             self._last, self._raw = s, s.cuda_stream
 
     def __call__(self, stream=None):

@@ -15,6 +15,8 @@ constexpr int kMaxV = 327680;
 constexpr int kMaxBias = 4096;
 constexpr int kMaxHistory = 1 << 23;   // counts are kept in 23 bits
 constexpr int kMaxGridYZ = 65535;
+constexpr int64_t kMaxTokens = 1 << 30;        // of one sequence's page table
+constexpr int64_t kMaxStride = 1ll << 39;      // elements: a tensor map's strides stay below 2^40 bytes
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 svd_status from_cuda(int err) { return err == 0 ? SVD_OK : SVD_ERR_CUDA; }
@@ -62,7 +64,7 @@ svd_status run_logits(const svd_logits_process_args* a, bool grad, bool aligned,
 bool bad_pages(int n_pages, int page_size, int max_pages, const void* ck, const void* cv,
                const int32_t* table, int64_t sk, int64_t sv, int64_t page_elems) {
     if (n_pages < 0 || max_pages < 0 || page_size < 1) return true;
-    if (static_cast<int64_t>(max_pages) * page_size > INT32_MAX) return true;
+    if (static_cast<int64_t>(max_pages) * page_size > kMaxTokens) return true;
     if (max_pages > 0 && !table) return true;
     if (n_pages > 0 && (!ck || !cv)) return true;
     // pages that overlap or lie backwards make no cache
@@ -90,6 +92,9 @@ svd_status svd_tree_attention(const svd_tree_attention_args* a, void* ws, size_t
                   a->page_stride_k, a->page_stride_v,
                   static_cast<int64_t>(a->page_size) * a->Hkv * a->D))
         return SVD_ERR_INVALID_ARG;
+    if (a->page_stride_k >= kMaxStride || a->page_stride_v >= kMaxStride ||
+        static_cast<int64_t>(a->page_size) * a->Hkv * a->D >= kMaxStride)
+        return SVD_ERR_UNSUPPORTED;
     if (a->D > 128 || a->D % 8 != 0 || a->Hq > 1024 || a->page_size < 8 || (a->page_size & (a->page_size - 1)) != 0)
         return SVD_ERR_UNSUPPORTED;
     if (a->B == 0) return SVD_OK;

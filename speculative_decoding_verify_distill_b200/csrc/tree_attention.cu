@@ -7,25 +7,29 @@
 // arithmetic behind it; with more rows the softmax bounds it (16 exponentials a clock and SM).
 //
 // Work.  An item is one sequence and key head; its keys are tiles of 128: the cached ones, then one tile of
-// the drafted nodes.  All tiles of all items form one line (with a few places for the start and end of each
-// item) that is cut into equal parts, so ragged lengths balance by themselves and one long sequence spreads over the whole GPU.  A CTA takes one part for
-// one group of 128 query rows (a row is a node and a query head); the CTAs of the same part and different
-// groups run side by side and share the part's keys through L2.  A part that holds a whole item writes its
-// result; otherwise it leaves the unnormalised sum with the row maxima and sums in the workspace, and a
-// second kernel (a programmatic dependent, its launch hidden) joins the parts in a fixed order.
+// the drafted nodes.  All tiles of all items form one line (with a few places for the start and end of
+// each item) that is cut into equal parts, so ragged lengths balance by themselves and one long sequence
+// spreads over the whole GPU.  A CTA takes one part for one group of 128 query rows (a row is a node and a
+// query head); the CTAs of the same part and different groups run side by side and share the part's keys
+// through L2.  A part that holds a whole item writes its result; otherwise it leaves the unnormalised sum with
+// the row maxima and sums in the workspace, and a second kernel (a programmatic dependent, its launch hidden)
+// joins the parts in a fixed order.
 //
-// Roles in a CTA.  A producer warp loads K and V tiles page by page by TMA (128-byte swizzle) into a
-// ring; one warp issues tcgen05.mma: S = Q K^T into one of three TMEM slots, up to two tiles ahead, and
-// O += P V with P read from TMEM; two softmax warpgroups take the tiles in turn, thread = row, so the
-// sums and maxima of a tile need no exchange.  A warpgroup reads S and moves the row's reference maximum
-// only when a tile exceeds it by more than 2^8 (the sums and O share the stale reference, so the quotient
-// is exact all the same, and O in TMEM is rescaled rarely), hands the reference to the other warpgroup, and
-// writes P = exp2(S - m) over S in the tensors' type (that rounding, at most half a step of the type
-// per weight, is what the matrix instruction takes; maxima and sums stay fp32).  A warp needs about 2200
-// cycles for a tile, of which 1024 are its exponentials, and a tile's bytes take 2800 at HBM's rate: one
-// warpgroup alone was too slow beside the waits, and so were two that split the columns.  Where an item
-// ends, Q of the next one is fetched behind the last tile's softmax, and its first S forms while O is
-// written out.
+// Roles in a CTA.  Two warps load K and V tiles page by page by TMA (128-byte swizzle), each into a ring of
+// its own.  Two warps issue tcgen05.mma: one S = Q K^T into the next of three TMEM slots as soon as it is
+// free, one O += P V with P read from TMEM.  Two softmax warpgroups take the tiles in turn, thread = row, so
+// the sums and maxima of a tile need no exchange.  A warpgroup reads S and moves the row's reference maximum
+// only when a tile exceeds it by more than 2^8 (the sums and O share the stale reference, so the quotient is
+// exact all the same, and O in TMEM is rescaled rarely), hands the reference to the other warpgroup, and
+// writes P = exp2(S - m) over S in the tensors' type (that rounding, at most half a step of the type per
+// weight, is what the matrix instruction takes; maxima and sums stay fp32).  Where an item ends, Q of the next
+// one is fetched behind the last tile's softmax, and its first S forms while O is written out.
+//
+// Why so (cycles a tile, heads of 128; a tile's bytes take 2800 at HBM's rate and 1965 MHz): one softmax
+// warpgroup alone took 1850 to 2200 besides its waits, of which 1024 are exponentials, and two that split the
+// columns lost as much to their exchange; one warp for all products was busy 2300, most of it with waits; one
+// warp for all loads 3200 where pages have 16 tokens.  As it is a tile takes about 1200 to 1700, so a cache
+// streams at the rate of HBM: 6000 tokens of 128 sequences at 6.8 TB/s.
 //
 // Masks.  Columns behind the cache length and nodes that are not ancestors get P = 0 whatever S
 // holds.  0 * NaN would still reach O through the matrix product, so rows of V behind the length

@@ -190,6 +190,20 @@ def test_attention_items_of_one_tile(n, Hq, Hkv, D, dtype):
     assert all(torch.equal(v, first[k]) for k, v in op.outputs().items())
 
 
+def test_attention_parts_of_many_sequences():
+    """More sequences in a part than a part keeps lengths of; one key each, so out is v and lse is the score."""
+    B, D = 12001, 64
+    g = gen(20)
+    q, k, v = (torch.randn((B, 1, 1, D), generator=g, device="cuda").to(BF) for _ in range(3))
+    empty = torch.empty((0, 16, 1, D), dtype=BF, device="cuda")
+    out = api.svd_tree_attention(q, k, v, empty, empty, torch.empty((B, 0), dtype=I32, device="cuda"),
+                                 torch.zeros(B, dtype=I32, device="cuda"), lse=True)
+    assert torch.equal(out["out"], v)
+    s = (q.double() * k.double()).sum(-1) / 8
+    mag = (q.double() * k.double()).abs().sum(-1) / 8
+    assert ((out["lse"].double() - s).abs() <= 2.0 ** -23 * D * mag + 2.0 ** -21 * s.abs() + 2.0 ** -21).all()
+
+
 def test_attention_more_row_groups_than_sms():
     """One key head for 1024 query heads of 20 nodes: 160 groups of 128 rows."""
     check_attention(attention_case([300, 7], 20, 1024, 1, 64, 32, seed=19))
@@ -367,6 +381,53 @@ def test_process_values_that_are_not_numbers():
     zeros[0, 0, :5] = -0.0
     zeros[0, 0, 9] = 0.0
     assert api.svd_logits_process(zeros, argmax=True)["argmax"].item() == 0
+
+
+def shifted(t, by=1):
+    """The same values at an address that is not 16-byte aligned."""
+    buf = torch.empty(t.numel() + by, dtype=t.dtype, device=t.device)
+    return buf[by:].view(t.shape).copy_(t)
+
+
+def test_tensors_that_are_not_aligned():
+    logits, c = process_case(3, 5, 2056, 40, 6, "row", seed=13)
+    want = check_process(logits, c)
+    got = check_process(shifted(logits), c, out=shifted(torch.empty_like(logits)))
+    assert torch.equal(got["out"], want["out"]) and torch.equal(got["argmax"], want["argmax"])
+    dz = torch.randn((3, 5, 2056), generator=gen(3), device="cuda")
+    g = {k: v for k, v in c.items() if k not in ("frequency", "presence")}
+    a = api.svd_logits_process_grad(dz, logits, **g)["dlogits"]
+    assert torch.equal(api.svd_logits_process_grad(shifted(dz), shifted(logits), **g)["dlogits"], a)
+    tok = c["node_tok"]
+    a, b = (api.svd_tree_verify(tok, logits=x, parent=c["parent"]) for x in (logits, shifted(logits)))
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    t = attention_case([20], 2, 4, 2, 64, 16, seed=1)
+    for name in ("q", "k_new", "cache_v"):
+        x = {**t, name: shifted(t[name])}
+        with pytest.raises(api.SvdError) as e:
+            api.svd_tree_attention(*[x[k] for k in ("q", "k_new", "v_new", "cache_k", "cache_v", "page_table", "cache_len")])
+        assert e.value.code == 2
+
+
+def test_refused_tensors():
+    """Types, shapes and strides that the entry points do not take."""
+    t = attention_case([20, 30], 2, 4, 2, 64, 16, seed=1)
+    names = ("q", "k_new", "v_new", "cache_k", "cache_v", "page_table", "cache_len")
+    for name, bad in (("k_new", t["k_new"].half()), ("cache_k", t["cache_k"].float()), ("page_table", t["page_table"].long()),
+                      ("cache_len", t["cache_len"][:1]), ("q", t["q"].transpose(1, 2)), ("v_new", t["v_new"][:, :1]),
+                      ("cache_v", t["cache_v"].transpose(1, 2)), ("cache_v", t["cache_v"][:3]), ("cache_len", t["cache_len"].cpu())):
+        with pytest.raises((TypeError, ValueError)):
+            api.TreeAttention(*[{**t, name: bad}[k] for k in names])
+    with pytest.raises(ValueError):
+        api.TreeAttention(*[t[k] for k in names], parent=t["parent"][:1])
+    for kw, code in ((dict(scale=math.inf), 1),):
+        with pytest.raises(api.SvdError) as e:
+            api.svd_tree_attention(*[t[k] for k in names], **kw)
+        assert e.value.code == code
+    wide = attention_case([20], 2, 2, 1, 136, 16, seed=1)
+    with pytest.raises(api.SvdError) as e:
+        api.svd_tree_attention(*[wide[k] for k in names])
+    assert e.value.code == 6
 
 
 def test_process_errors():

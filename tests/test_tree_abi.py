@@ -70,7 +70,7 @@ ATT = dict(q=FAKE, k_new=FAKE, v_new=FAKE, cache_k=FAKE, cache_v=FAKE, page_stri
 @pytest.mark.parametrize("kw,code", [
     (dict(n=0), 1), (dict(n=65), 1), (dict(B=-1), 1), (dict(Hq=9), 1), (dict(Hkv=0), 1), (dict(D=0), 1), (dict(dtype=2), 1),
     (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(n_pages=-1), 1), (dict(max_pages=-1), 1),
-    (dict(page_size=0), 1), (dict(max_pages=1 << 28), 1), (dict(page_table=None), 1), (dict(cache_k=None), 1),
+    (dict(page_size=0), 1), (dict(max_pages=1 << 28), 1), (dict(max_pages=(1 << 26) + 1), 1), (dict(page_stride_k=1 << 39), 6), (dict(page_table=None), 1), (dict(cache_k=None), 1),
     (dict(page_stride_k=16 * 4 * 64 - 8), 1), (dict(page_stride_v=-8), 1), (dict(q=None), 1), (dict(k_new=None), 1),
     (dict(cache_len=None), 1), (dict(out=None), 1), (dict(D=136, page_stride_k=BIG, page_stride_v=BIG), 6),
     (dict(D=60), 6), (dict(page_size=4), 6), (dict(page_size=24, page_stride_k=BIG, page_stride_v=BIG), 6), (dict(Hq=2048), 6),
