@@ -1,6 +1,7 @@
 """Python binding of ``libsvd.so`` -- argument marshalling only.
 
-Every entry point has the name of its C function in ``include/svd.h`` and calls it through
+Every entry point has the name of its C function in ``include/svd.h``, ``svd_vocab.h`` or
+``svd_tree.h`` and calls it through
 ctypes with device pointers taken from torch tensors and the current CUDA stream.  PyTorch is
 used for device memory and streams only; all arithmetic runs in the CUDA kernels.  There is no
 fallback: if the library is missing or no GPU is present the call raises.
