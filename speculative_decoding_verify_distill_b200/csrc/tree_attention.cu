@@ -148,7 +148,7 @@ struct Walker {
 
 struct Control {
     uint64_t full[2][6], empty[2][6];   // of the K ring, of the V ring
-    uint64_t s_full[3], p_full[3], pv_done[3], m_ready[4][2], pair[4], aux[2], q_full, drain[2];
+    uint64_t s_full[3], p_full[3], pv_done[3], m_ready[4][2], pair[4], aux[2], q_full, o_free, drain[2];
     long long lo, hi, base, total, parts;
     unsigned long long poison[2];  // drafted nodes with a V element that is not finite (alternating)
     int b;
@@ -280,6 +280,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
             mbar_init(&ctl.aux[0], 1);
             mbar_init(&ctl.aux[1], 1);
             mbar_init(&ctl.q_full, 8);
+            mbar_init(&ctl.o_free, 8);
             mbar_init(&ctl.drain[0], 1);
             mbar_init(&ctl.drain[1], 1);
             fence_mbar_init();
@@ -451,9 +452,9 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         // ------------------------------------------------------------------ O += P V
         constexpr uint32_t kId = mma_desc(FP16, true, kTile, DP);
         const bool one = lane == 0;
-        uint32_t u = 0, naux = 0;
+        uint32_t u = 0, naux = 0, seg = 0;
         bool ok = true;
-        while (ok && wk.next(p, ctl.lens)) {
+        for (; ok && wk.next(p, ctl.lens); ++seg) {
             for (int kt = s.tile0; ok && kt < s.tile1; ++kt, ++u) {
                 const uint32_t st = u % NS, slot = u % 3;
                 uint8_t* v = sm_kv + (NS + st) * Sh::kTileBytes;
@@ -507,6 +508,8 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                     __syncwarp();
                 }
                 ok = wait(&ctl.p_full[slot], u / 3);
+                // (P comes from one warpgroup; the other may still be reading the O of the segment before)
+                if (kt == s.tile0 && seg > 0) ok = ok && wait(&ctl.o_free, seg - 1);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t v_desc = mat_desc(smem_addr(v), kHalfBytes, 1024);
@@ -783,6 +786,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
             }
             tc_fence_before();
             __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.o_free);
         }
         // (a wait that ran out may have left some in flight)
         asm volatile("cp.async.wait_all;" ::: "memory");
