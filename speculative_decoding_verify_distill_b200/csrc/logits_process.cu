@@ -40,7 +40,6 @@ constexpr int kVecs = 2;                       // vectors of 8 ids per lane and 
 constexpr int kWarpIds = 8 * 32 * kVecs;       // ids of a warp
 constexpr int kChunk = kWarps * kWarpIds;      // ids per CTA
 constexpr int kStages = 2;
-constexpr int kAhead = 4;                      // pairs per lane whose raw logits the gradient loads ahead
 constexpr int kStageBytes = 4 * kChunk;        // two rows of bf16 or one of fp32
 constexpr int kFewCtas = 444;                  // three per SM
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -196,6 +195,10 @@ template <bool GRAD, bool F32, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 3) logits_process_kernel(LogitsParams p) {
     using T = typename std::conditional<F32, float, uint16_t>::type;
     constexpr int kRows = F32 ? 1 : 2;                    // rows per stage
+    // Pairs per lane that are worked on at once, and whose raw logits the gradient loads ahead: as many as a dense
+    // chunk's two rows need (8 x 64 rows in bf16: 89.1 us with four, 91.6 with two), but one row of fp32 has half of
+    // them (6 x 16 rows: 25.0 us with two, 26.7 with four).
+    constexpr int kAhead = F32 ? 2 : 4;
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ Tables s;
     const svd_logits_process_args& a = p.a;
