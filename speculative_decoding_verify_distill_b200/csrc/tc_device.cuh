@@ -8,19 +8,6 @@
 
 namespace svd {
 
-// Whether phase `parity` of `bar` has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
 // Box of a 4-dimensional tensor map to this CTA's shared memory (no multicast), issued by the lane that has
 // `one` set; c0 * element size is a multiple of 16 bytes.
 __device__ __forceinline__ void tma_load_4d(bool one, void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,

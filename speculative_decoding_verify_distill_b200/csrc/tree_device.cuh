@@ -43,7 +43,6 @@ __device__ __forceinline__ int argmax_id(unsigned long long key) {
     return key == 0ull ? 0 : static_cast<int>(~static_cast<uint32_t>(key));
 }
 
-// Largest of eight bf16 values (packed compares drop a NaN next to a number), NaN if all are.
 // Warp-wide: the key of the warp's best value over the vectors (`best`, ids from `at`) that its
 // lanes hold; 0 if there is none.  `has` is false for lanes without a vector.
 __device__ __forceinline__ unsigned long long warp_best_key(bool has, const uint4& best, int at) {

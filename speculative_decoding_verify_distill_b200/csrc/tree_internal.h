@@ -48,7 +48,6 @@ int launch_tree_verify(const VerifyParams& p, void* stream);
 // ------------------------------------------------------------------------------------------
 struct AppendParams {
     svd_cache_append_args a;
-    int entries_per_cta;
     uint32_t* status;
     uint32_t* ticket;
 };
