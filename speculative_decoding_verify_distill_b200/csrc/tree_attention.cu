@@ -22,7 +22,8 @@
 // only when a tile exceeds it by more than 2^8 (the sums and O share the stale reference, so the quotient is
 // exact all the same, and O in TMEM is rescaled rarely), hands the reference to the other warpgroup, and
 // writes P = exp2(S - m) over S in the tensors' type (that rounding, at most half a step of the type per
-// weight, is what the matrix instruction takes; maxima and sums stay fp32).  Where an item ends, Q of the next
+// weight, is what the matrix instruction takes; maxima and sums stay fp32).  In fp16 the weights carry a factor of
+// 2^7, see kLift.  Where an item ends, Q of the next
 // one is fetched behind the last tile's softmax, and its first S forms while O is written out.
 //
 // Why so (cycles a tile, heads of 128; a tile's bytes take 2800 at HBM's rate and 1965 MHz): one softmax
@@ -163,6 +164,16 @@ template <bool FP16>
 __device__ __forceinline__ float to_f32(uint16_t w) {
     return FP16 ? __half2float(__ushort_as_half(w)) : __uint_as_float(static_cast<uint32_t>(w) << 16);
 }
+// Weights are 2^kLift exp2(S - m), the factor with them in the sums and in O: it cancels in the quotient, and
+// lse takes it back.  fp16 has no normal values below 2^-14 and none below 2^-24, so without it a weight below 2^-25 of the
+// largest was lost in O but not in the sum: under one dominant key the share of 32768 others was off by 6% where they
+// were e^-16 each, and lost whole from e^-17.5 on.  The stale reference lets weights grow by 2^8, to 2^15 < 65504.
+// What is left is 2^-32 of the largest weight for each key, in sum half a step of fp16 at 2^21 keys.
+template <bool FP16>
+constexpr float kLift = FP16 ? 7.f : 0.f;
+template <bool FP16>
+constexpr float kUnlift = FP16 ? 0x1p-7f : 1.f;
+
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if (!FP16) return pack_bf16x2(lo, hi);
@@ -201,7 +212,7 @@ __device__ __noinline__ void add_not_finite(const AttnParams& p, unsigned long l
         for (int d = 0; d < a.D; ++d) dot += to_f32<FP16>(qr[d]) * to_f32<FP16>(kr[d]);
         dot = p.qzero ? 0.f : (p.qflip ? -dot : dot);
         // (a weight that underflows is not zero)
-        const float w = fmaxf(fast_exp2((dot - m) * p.c) * factor, 1e-30f);
+        const float w = fmaxf(fast_exp2((dot - m) * p.c + kLift<FP16>) * factor, 1e-30f);
 #pragma unroll 1
         for (int d = d0; d < d1; ++d) {
             const float x = to_f32<FP16>(vr[d]);
@@ -681,7 +692,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                     if (lane == 0) mbar_arrive(&ctl.m_ready[quarter][wg]);
                     if (__any_sync(0xffffffffu, m != mn)) l *= m == mn ? 1.f : fast_exp2((m - mn) * c);
                     m = mn;
-                    const float mref = m == -INFINITY ? 0.f : -m * c;
+                    const float mref = m == -INFINITY ? 0.f : kLift<FP16> - m * c;
                     const float2 c2 = make_float2(c, c), m2 = make_float2(mref, mref);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
@@ -781,7 +792,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
                 __syncwarp();
                 if (live && wg == 0) {
                     if (!whole) p.ml[slot] = make_float2(m, l);
-                    else if (a.lse) a.lse[qrow] = pad ? -INFINITY : (m == -INFINITY ? 0.f : m * c * kLn2) + logf(l);
+                    else if (a.lse) a.lse[qrow] = pad ? -INFINITY : (m == -INFINITY ? 0.f : m * c * kLn2) + logf(l * kUnlift<FP16>);
                 }
             }
             tc_fence_before();
@@ -841,7 +852,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
         if (pad) w = make_uint2(0u, 0u);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qrow * a.D + lane * 4) = w;
     }
-    if (a.lse && lane == 0) a.lse[qrow] = pad ? -INFINITY : (m == -INFINITY ? 0.f : m * p.c * kLn2) + logf(l);
+    if (a.lse && lane == 0) a.lse[qrow] = pad ? -INFINITY : (m == -INFINITY ? 0.f : m * p.c * kLn2) + logf(l * kUnlift<FP16>);
 }
 
 // The driver's encoder, reached through the runtime so that the library does not link the driver.

@@ -1,0 +1,73 @@
+"""Edges of the operators on a tree of drafts: very small softmax weights, values that are not finite
+across parts, padding, streams, captured calls, and workspaces between calls."""
+import math
+
+import pytest
+import torch
+
+from speculative_decoding_verify_distill_b200 import api
+from tests import tree_ref as R
+from tests.test_gpu_tree_ops import (BF, FP, I32, attention_case, check_attention, first_argmax, gen, ints,
+                                     process_case)
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+ATT = ("q", "k_new", "v_new", "cache_k", "cache_v", "page_table", "cache_len")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from speculative_decoding_verify_distill_b200 import build
+    build.build()
+
+
+def copies(op):
+    return {k: v.clone() for k, v in op.outputs().items()}
+
+
+def same_bits(a, b):
+    view = {2: torch.int16, 4: torch.int32}
+    return all(torch.equal(v.view(view[v.element_size()]), b[k].view(view[v.element_size()])) for k, v in a.items())
+
+
+# ------------------------------------------------------------------------------------------
+# attention
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("B", [148, 1])
+@pytest.mark.parametrize("gap", [8.0, 12.0, 14.0, 16.0, 17.5, 19.0])
+def test_attention_one_large_weight_and_a_long_tail(gap, B, dtype):
+    """One key takes nearly all of the weight and 32767 others share e^-gap each: what they add up to must not
+    be lost where a weight is rounded to 16 bits.  All sequences read the same pages, so that with 148 of
+    them a whole sequence is one part.
+
+    A weight 2^z, relative to the row's largest, goes into the product as 2^(z + 7) in fp16: it is off by half a step
+    (2^-11 of itself), or by half of the smallest step, 2^-25, which is 2^-32 of the largest weight; in bf16 by
+    half a step alone (2^-8).  Scores are exact here; exp2 and the scaling to base 2 are off by
+    e = 2^-21 + 2^-22 gap, the sum over T keys by T 2^-24 of itself, and the result is rounded once."""
+    L, D, page = 32768, 64, 128
+    dev = "cuda"
+    k, v = torch.zeros((L, D), device=dev), torch.randn((L, D), generator=gen(31), device=dev).abs() + 0.25
+    k[1:, 0] = -gap
+    v[0] = 0
+    q = torch.zeros((B, 1, 1, D), device=dev)
+    q[..., 0] = 1
+    k_new, v_new = torch.zeros((B, 1, 1, D), device=dev), torch.ones((B, 1, 1, D), device=dev)
+    k_new[..., 0] = -gap
+    k, v, q, k_new, v_new = (x.to(dtype) for x in (k, v, q, k_new, v_new))
+    table = torch.arange(L // page, device=dev, dtype=I32).expand(B, -1).contiguous()
+    op = api.TreeAttention(q, k_new, v_new, k.view(-1, page, 1, D), v.view(-1, page, 1, D), table,
+                           torch.full((B,), L, dtype=I32, device=dev), scale=1.0, lse=True)
+    out = op().outputs()
+    assert op.device_error() == 0
+    w = torch.exp(torch.cat([k[:, 0], k_new[0, 0, 0, :1]]).double())
+    vv = torch.cat([v, v_new[0, 0]]).double()
+    l, T = w.sum(), L + 1
+    want, mag = w @ vv / l, w @ vv.abs() / l
+    u, e = torch.finfo(dtype).eps / 2, 2.0 ** -21 + 2.0 ** -22 * gap
+    small = 2.0 ** -32 if dtype == FP else 0.0
+    out_step = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps / 2
+    tol = u * want + mag * (u + 2 * e + T * 2.0 ** -24) + small * vv.abs().sum(0) / l + out_step
+    got = out["out"].double().view(B, D)
+    assert ((got - want).abs() <= tol).all(), ((got - want).abs() / want).max().item()
+    assert ((out["lse"].double() - l.log()).abs() <= 2 * e + T * 2.0 ** -24 + 2.0 ** -22 * l.log().abs()).all()
