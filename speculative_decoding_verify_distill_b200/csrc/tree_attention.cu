@@ -840,7 +840,11 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
         l += ml.y * f;
         if (act) {
             const float4 o = *reinterpret_cast<const float4*>(p.o + slot(i) * a.D + lane * 4);
-            acc.x += o.x * f; acc.y += o.y * f; acc.z += o.z * f; acc.w += o.w * f;
+            // an infinity of a visible node stays one where the part lies so far below the maximum that f is zero
+            acc.x += isinf(o.x) ? o.x : o.x * f;
+            acc.y += isinf(o.y) ? o.y : o.y * f;
+            acc.z += isinf(o.z) ? o.z : o.z * f;
+            acc.w += isinf(o.w) ? o.w : o.w * f;
         }
     }
     const int node = row / p.G, head = inf.hk * p.G + row - node * p.G;

@@ -71,3 +71,32 @@ def test_attention_one_large_weight_and_a_long_tail(gap, B, dtype):
     got = out["out"].double().view(B, D)
     assert ((got - want).abs() <= tol).all(), ((got - want).abs() / want).max().item()
     assert ((out["lse"].double() - l.log()).abs() <= 2 * e + T * 2.0 ** -24 + 2.0 ** -22 * l.log().abs()).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("L,B", [(100, 1), (100, 148), (700, 1), (20000, 1)])
+def test_attention_infinite_drafted_value_far_below_the_maximum(L, B, bad, dtype):
+    """A drafted value that is not finite reaches the rows that see its node, however small the node's weight is and
+    however the sequence was cut into parts (148 short ones are a part each): the scores of all cached keys but the last 300 lie 200 above."""
+    c = attention_case([L] * B, 3, 2, 1, 64, 16, dtype, seed=32, kind="chain")
+    c["page_table"][:] = c["page_table"][0].clone()
+    t = torch.arange(L, device="cuda")
+    c["q"], c["k_new"] = torch.zeros_like(c["q"]), torch.zeros_like(c["k_new"])
+    c["q"][..., 0] = 20
+    k = torch.zeros((L, 1, 64), device="cuda")
+    k[:max(1, L - 300), 0, 0] = 10
+    c["cache_k"][c["page_table"][0].long()[t // 16], t % 16] = k.to(dtype)
+    clean = copies(check_attention(c, scale=1.0))
+    assert (clean["lse"] >= 199).all()
+    c["v_new"] = c["v_new"].clone()
+    c["v_new"][:, 1, 0, 5:40] = bad
+    op = api.TreeAttention(*[c[x] for x in ATT], parent=c["parent"], scale=1.0, lse=True)
+    out = op().outputs()
+    assert op.device_error() == 0
+    assert torch.equal(out["lse"], clean["lse"])
+    hit = torch.zeros((B, 3, 2, 64), dtype=torch.bool, device="cuda")
+    hit[:, 1:, :, 5:40] = True
+    assert torch.equal(out["out"][~hit], clean["out"][~hit])
+    got = out["out"][hit].float()
+    assert got.isnan().all() if math.isnan(bad) else (got == bad).all()
