@@ -14,7 +14,8 @@
  *     was emitted last and is not yet in the cache.  Row j of the logits is the target's
  *     distribution after node j.
  *   - n_nodes[b] <= n nodes are in use (NULL: all n); the others are padding.
- *   - A parent outside [-1, j) counts as -1 and records SVD_ERR_TREE.
+ *   - A parent outside [-1, j) of a node in use counts as -1 and records SVD_ERR_TREE; parents of
+ *     padding nodes are not read.  (The processing of logits has no n_nodes: all its nodes are in use.)
  *
  * The paged cache
  *   - cache_k and cache_v hold n_pages pages of page_size tokens, [page_size, Hkv, D] each,

@@ -606,8 +606,8 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
             const bool has_new = s.tile1 == s.tiles;
             if (has_new && warp_live && s.b != anc_seq) {
                 const size_t at = static_cast<size_t>(s.b) * a.n;
-                const int p0 = lane < a.n ? checked_parent(a.parent, at, lane, p.status) : -1;
-                const int p1 = lane + 32 < a.n ? checked_parent(a.parent, at, lane + 32, p.status) : -1;
+                const int p0 = lane < used ? checked_parent(a.parent, at, lane, p.status) : -1;
+                const int p1 = lane + 32 < used ? checked_parent(a.parent, at, lane + 32, p.status) : -1;
                 int i = live && node < used ? node : -1;
                 anc = 0;
                 while (__any_sync(0xffffffffu, i >= 0)) {

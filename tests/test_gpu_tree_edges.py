@@ -100,3 +100,18 @@ def test_attention_infinite_drafted_value_far_below_the_maximum(L, B, bad, dtype
     assert torch.equal(out["out"][~hit], clean["out"][~hit])
     got = out["out"][hit].float()
     assert got.isnan().all() if math.isnan(bad) else (got == bad).all()
+
+
+def test_attention_parents_of_padding_nodes_are_not_read():
+    """What lies behind n_nodes may be anything, the parents too; a parent out of range of a node in use is recorded."""
+    c = attention_case([50, 0, 300, 20], 40, 8, 2, 64, 16, seed=33)
+    nn = ints([40, 33, 5, 0])
+    want = copies(check_attention(c, n_nodes=nn))
+    for b, m in enumerate(nn.tolist()):
+        c["parent"][b, m:] = 1 << 20
+        c["parent"][b, m + 1:] = -7
+    assert same_bits(check_attention(c, n_nodes=nn).outputs(), want)
+    c["parent"][1, 32] = 33
+    op = api.TreeAttention(*[c[x] for x in ATT], parent=c["parent"], n_nodes=nn)
+    op()
+    assert op.device_error() == 9
