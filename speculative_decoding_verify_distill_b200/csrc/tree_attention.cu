@@ -621,10 +621,12 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
             float m = -INFINITY, l = 0.f;
             const uint32_t u_end = u + static_cast<uint32_t>(s.tile1 - s.tile0);
             for (int kt = s.tile0; ok && kt < s.tile1; ++kt, ++u) {
-                // the last S of this segment is there: Q is free for the next one
+                // A segment's last S is waited for by both warpgroups: Q is free for the next segment, and the wait on
+                // pv_done[slot] below cannot pass on the phase before last (S of this tile was issued behind
+                // the product of the tile that had the slot before).
                 const bool last = kt + 1 == s.tile1, mine = (u & 1u) == wg;
                 const uint32_t slot = u % 3;
-                if (mine || (last && more)) ok = wait(&ctl.s_full[slot], u / 3);
+                if (mine || last) ok = wait(&ctl.s_full[slot], u / 3);
                 if (!ok) break;
                 if (last && more) fetch_q(wk.s);
                 if (mine && warp_live) {

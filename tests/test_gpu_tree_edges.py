@@ -115,3 +115,23 @@ def test_attention_parents_of_padding_nodes_are_not_read():
     op = api.TreeAttention(*[c[x] for x in ATT], parent=c["parent"], n_nodes=nn)
     op()
     assert op.device_error() == 9
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,D,page,dtype", [(1, 4, 1, 128, 16, BF), (33, 8, 2, 64, 64, FP), (64, 16, 2, 128, 32, BF)])
+def test_attention_of_parts_that_end_on_either_warpgroup(n, Hq, Hkv, D, page, dtype):
+    """Lengths at which parts hold one, two, three or more tiles, an odd or an even number: the results are right and the
+    same in every repeat."""
+    for lens in ([148 * 128 * k + d for k, d in ((1, 0), (1, -128), (2, 100), (3, 1))],
+                 [128 * i + 5 for i in range(9)] * 4, [4096] * 37):
+        if n > 1:
+            lens = [x // 4 for x in lens]
+        c = attention_case(lens[:2] if n > 1 and max(lens) > 5000 else lens, n, Hq, Hkv, D, page, dtype, seed=34)
+        if n > 1 and len(c["cache_len"]) > 4:
+            op = api.TreeAttention(*[c[x] for x in ATT], parent=c["parent"], lse=True)()
+        else:
+            op = check_attention(c)
+        first = copies(op)
+        for _ in range(30):
+            op()
+        assert same_bits(op.outputs(), first)
+        assert op.device_error() == 0
