@@ -697,6 +697,13 @@ class _TreeOp:
             s = self._last if stream is None else stream
             return int(lib().svd_get_device_error(self._ws, s.cuda_stream))
 
+    def reset(self):
+        """Zeroes the workspace, the status word with it, on the stream of the last call
+        (``svd_workspace_reset``): for use after a device error."""
+        with torch.cuda.device(self.device):
+            _check(lib().svd_workspace_reset(self._ws, self._nws, self._last.cuda_stream), "svd_workspace_reset")
+        return self
+
 
 def _once(op, args, kw, stream):
     """One call of a fresh object, with its buffers allocated on the stream that it runs on."""

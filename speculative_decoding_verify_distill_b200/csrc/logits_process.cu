@@ -479,12 +479,11 @@ __global__ void __launch_bounds__(kThreads, 3) logits_process_kernel(LogitsParam
             set_device_error(p.status, SVD_ERR_TIMEOUT);
             for (int i = 0; i < kStages; ++i) mbar_wait_bounded(&s.full[i], 0, kWaitNs), mbar_wait_bounded(&s.full[i], 1, kWaitNs);
         }
-        return;
     }
     if (!want_arg) return;
     // one atomic maximum per row and CTA (a maximum does not depend on the order); the last CTA of
-    // the sequence turns the keys into ids and leaves the workspace zero
-    if (t < j1 - j0) {
+    // the sequence turns the keys into ids and leaves the workspace zero, behind a time-out too
+    if (ok && t < j1 - j0) {
         unsigned long long key = 0;
         for (int w = 0; w < kWarps; ++w) {
             if (s.best_at[w][t] < 0) continue;

@@ -135,3 +135,53 @@ def test_attention_of_parts_that_end_on_either_warpgroup(n, Hq, Hkv, D, page, dt
             op()
         assert same_bits(op.outputs(), first)
         assert op.device_error() == 0
+
+
+# ------------------------------------------------------------------------------------------
+# workspaces, streams and graphs
+# ------------------------------------------------------------------------------------------
+def handles():
+    """An object of every operator whose workspace holds keys or tickets between its blocks."""
+    logits, c = process_case(4, 9, 5000, 200, 10, "row", seed=40)
+    g = gen(41)
+    T = torch.randn((3, 12, 20000), generator=g, device="cuda").to(BF)
+    parent = R.random_tree(3, 12, 41).cuda()
+    y = first_argmax(T)
+    tok = torch.where(torch.rand((3, 12), generator=g, device="cuda") < 0.8, y.gather(1, parent.clamp(min=0).long()), 0).to(I32)
+    k, v = (torch.randn((5, 21, 2, 64), generator=g, device="cuda").to(BF) for _ in range(2))
+    cache = [torch.zeros((5 * 8, 8, 2, 64), dtype=BF, device="cuda") for _ in range(2)]
+    table = torch.randperm(40, generator=g, device="cuda").to(I32).view(5, 8)
+    return [api.LogitsProcess(logits, argmax=True, **c), api.LogitsProcess(logits, argmax=True, values=False, **c),
+            api.TreeVerify(tok, logits=T, parent=parent),
+            api.CacheAppend(k, v, *cache, table, ints([0, 3, 17, 8, 43]), ints([21, 0, 13, 5, 1]))]
+
+
+def wipe(op):
+    for t in op.outputs().values():
+        t.view(torch.int16 if t.element_size() == 2 else torch.int32).fill_(0x55)
+
+
+def wiped_cache(op):
+    """The cache keeps what a call does not write."""
+    if isinstance(op, api.CacheAppend):
+        op.cache_k.zero_()
+        op.cache_v.zero_()
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_workspace_is_ready_after_every_call_and_after_a_reset(which):
+    """Behind the header everything is zero again after a call.  Keys and tickets that were left by a call that did not end
+    spoil the next one, until the workspace is reset."""
+    op = handles()[which]
+    want = copies(op())
+    assert op.device_error() == 0 and not op.ws[256:].any()
+    op.ws[:4] = 5                      # a recorded time-out
+    op.ws[256:] = 1                    # ... and counts of blocks that had already run
+    assert op.reset() is op
+    assert not op.ws.any() and op.device_error() == 0
+    for _ in range(3):
+        wipe(op)
+        wiped_cache(op)
+        op()
+        assert same_bits(op.outputs(), want)
+    assert op.device_error() == 0 and not op.ws[256:].any()
