@@ -672,10 +672,14 @@ class _TreeOp:
             capturing = torch.cuda.is_current_stream_capturing()
         if not capturing:
             s.wait_stream(self._last)
-            for t in [self.ws, *self._keep, *self.outputs().values()]:
-                if t is not None:
-                    t.record_stream(s)
+            self._record(s)
             self._last, self._raw = s, s.cuda_stream
+
+    def _record(self, s):
+        """The memory of this object's tensors is not handed out again before the work on s has ended."""
+        for t in [self.ws, *self._keep, *self.outputs().values()]:
+            if t is not None:
+                t.record_stream(s)
 
     def __call__(self, stream=None):
         # the raw handle is enough while the stream stays the same (a Stream object costs 2 us)
@@ -706,11 +710,15 @@ class _TreeOp:
 
 
 def _once(op, args, kw, stream):
-    """One call of a fresh object, with its buffers allocated on the stream that it runs on."""
+    """One call of a fresh object, with its buffers allocated on the stream that it runs on.  The caller orders a
+    ``stream`` behind the work that made the inputs, but may let go of them as soon as the call returns."""
     if stream is None:
         return op(*args, **kw)().outputs()
     with torch.cuda.stream(stream):
-        return op(*args, **kw)(stream).outputs()
+        once = op(*args, **kw)(stream)
+        if not torch.cuda.is_current_stream_capturing():
+            once._record(stream)
+        return once.outputs()
 
 
 class TreeAttention(_TreeOp):

@@ -185,3 +185,26 @@ def test_workspace_is_ready_after_every_call_and_after_a_reset(which):
         op()
         assert same_bits(op.outputs(), want)
     assert op.device_error() == 0 and not op.ws[256:].any()
+
+
+def test_one_call_on_a_stream_keeps_its_inputs():
+    """Tensors that nobody else holds are not handed out again before the call on the side stream has read them."""
+    logits, c = process_case(2, 8, 100000, 50, 4, "row", seed=44)
+    want = copies(api.LogitsProcess(logits, argmax=True, **c)())
+    t = attention_case([500, 90], 4, 8, 2, 128, 16, seed=45)
+    att = copies(api.TreeAttention(*[t[x] for x in ATT], parent=t["parent"])())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        a, b = logits.clone(), {k: t[k].clone() for k in ATT[:5]}
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)
+        got = api.svd_logits_process(a, stream=side, argmax=True, **c)
+        out = api.svd_tree_attention(*b.values(), t["page_table"], t["cache_len"], parent=t["parent"], stream=side)
+        del a, b
+        # as large as what was let go, and filled before the side stream gets to its calls
+        spoil = [torch.full_like(logits, 77.0)] + [torch.full_like(t[k], 1) for k in ATT[:5]]
+        torch.cuda.synchronize()
+        assert same_bits(got, want) and same_bits(out, att)
+        del spoil
