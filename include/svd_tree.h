@@ -77,7 +77,7 @@ typedef struct svd_tree_attention_args {
     int B, n, Hq, Hkv, D;
     int n_pages, page_size, max_pages;
     svd_dtype dtype;            /* of q, k_new, v_new, the cache and out                       */
-    float scale;                /* finite                                                      */
+    float scale;                /* at most 2^127 in size                                       */
     void* out;                  /* [B, n, Hq, D]                                               */
     float* lse;                 /* [B, n, Hq] or NULL                                          */
 } svd_tree_attention_args;

@@ -87,7 +87,7 @@ svd_status svd_tree_attention(const svd_tree_attention_args* a, void* ws, size_t
     if (a->B < 0 || a->n < 1 || a->n > kTreeMaxNodes || a->Hkv < 1 || a->Hq < 1 || a->Hq % a->Hkv != 0 || a->D < 1)
         return SVD_ERR_INVALID_ARG;
     if (a->dtype != SVD_BF16 && a->dtype != SVD_FP16) return SVD_ERR_INVALID_ARG;
-    if (!std::isfinite(a->scale)) return SVD_ERR_INVALID_ARG;
+    if (!(std::fabs(a->scale) <= 0x1p127f)) return SVD_ERR_INVALID_ARG;   // scale * log2(e) stays finite
     if (bad_pages(a->n_pages, a->page_size, a->max_pages, a->cache_k, a->cache_v, a->page_table,
                   a->page_stride_k, a->page_stride_v,
                   static_cast<int64_t>(a->page_size) * a->Hkv * a->D))
