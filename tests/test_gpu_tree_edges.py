@@ -78,7 +78,8 @@ def test_attention_one_large_weight_and_a_long_tail(gap, B, dtype):
 @pytest.mark.parametrize("L,B", [(100, 1), (100, 148), (700, 1), (20000, 1)])
 def test_attention_infinite_drafted_value_far_below_the_maximum(L, B, bad, dtype):
     """A drafted value that is not finite reaches the rows that see its node, however small the node's weight is and
-    however the sequence was cut into parts (148 short ones are a part each): the scores of all cached keys but the last 300 lie 200 above."""
+    however the sequence was cut into parts (148 short ones are a part each): the scores of all cached keys but the
+    last 300 lie 200 above."""
     c = attention_case([L] * B, 3, 2, 1, 64, 16, dtype, seed=32, kind="chain")
     c["page_table"][:] = c["page_table"][0].clone()
     t = torch.arange(L, device="cuda")
@@ -187,6 +188,60 @@ def test_workspace_is_ready_after_every_call_and_after_a_reset(which):
     assert op.device_error() == 0 and not op.ws[256:].any()
 
 
+@pytest.mark.parametrize("which", range(4))
+def test_streams_and_captured_calls(which):
+    """Two objects on two streams at once, then both captured into a graph and replayed: every output is written
+    again, with the bits of the first call."""
+    ops = [handles()[which] for _ in range(2)]
+    want = [copies(op()) for op in ops]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for op in ops:
+        wipe(op)
+        wiped_cache(op)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for op, s in zip(ops, streams):
+            op(s)
+    torch.cuda.synchronize()
+    for op, w in zip(ops, want):
+        assert same_bits(op.outputs(), w) and op.device_error() == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for op in ops:
+            op()
+    for _ in range(3):
+        for op in ops:
+            wipe(op)
+            wiped_cache(op)
+        graph.replay()
+        torch.cuda.synchronize()
+        for op, w in zip(ops, want):
+            assert same_bits(op.outputs(), w)
+    for op in ops:
+        assert op.device_error(torch.cuda.current_stream()) == 0 and not op.ws[256:].any()
+
+
+def test_gradient_streams_and_captured_calls():
+    logits, c = process_case(4, 9, 5000, 200, 0, "row", seed=42)
+    c = {k: v for k, v in c.items() if k not in ("frequency", "presence")}
+    for dtype in (BF, torch.float32):
+        dz = torch.randn(logits.shape, generator=gen(43), device="cuda").to(dtype)
+        op = api.LogitsProcessGrad(dz, logits, **c)
+        want = copies(op())
+        wipe(op)
+        torch.cuda.synchronize()
+        op(torch.cuda.Stream())
+        torch.cuda.synchronize()
+        assert same_bits(op.outputs(), want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            op()
+        wipe(op)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same_bits(op.outputs(), want) and op.device_error() == 0
+
+
 def test_one_call_on_a_stream_keeps_its_inputs():
     """Tensors that nobody else holds are not handed out again before the call on the side stream has read them."""
     logits, c = process_case(2, 8, 100000, 50, 4, "row", seed=44)
@@ -208,3 +263,64 @@ def test_one_call_on_a_stream_keeps_its_inputs():
         torch.cuda.synchronize()
         assert same_bits(got, want) and same_bits(out, att)
         del spoil
+
+
+def test_attention_infinite_keys():
+    """A drafted key with an infinite element: a row that sees it with the score -inf is as if the node were not
+    there, one with the score +inf is not a number (inf - inf in every softmax)."""
+    c = attention_case([50, 0, 300], 12, 8, 2, 64, 16, seed=35)
+    c["q"][..., 0] = 1.0
+    par = c["parent"].tolist()
+    k_new = c["k_new"].clone()
+    k_new[:, 4, :, 0] = -math.inf
+    run = lambda k: api.svd_tree_attention(c["q"], k, *[c[x] for x in ATT[2:]], parent=c["parent"], lse=True)  # noqa: E731
+    clean, low = run(c["k_new"]), run(k_new)
+    k_new[:, 4, :, 0] = math.inf
+    high = run(k_new)
+    for b in range(3):
+        for j in range(12):
+            anc = R.ancestors(par[b], j)
+            if 4 not in anc:
+                for got in (low, high):
+                    assert torch.equal(got["out"][b, j], clean["out"][b, j]) and torch.equal(got["lse"][b, j], clean["lse"][b, j])
+                continue
+            assert high["out"][b, j].isnan().all() and high["lse"][b, j].isnan().all()
+            # the row alone, over the cache and a chain of the other nodes it sees
+            rest = [i for i in anc if i != 4]
+            one = lambda t: t[b:b + 1, rest].contiguous()  # noqa: E731
+            o, l, to, tl = R.attention(c["q"][b:b + 1, [j] * len(rest)], one(c["k_new"]), one(c["v_new"]), c["cache_k"], c["cache_v"],
+                                       c["page_table"][b:b + 1], c["cache_len"][b:b + 1])
+            assert ((low["out"][b, j].double() - o[0, -1]).abs() <= to[0, -1]).all()
+            assert ((low["lse"][b, j].double() - l[0, -1]).abs() <= tl[0, -1]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_attention_parts_of_many_sequences_of_differing_lengths(dtype):
+    """More sequences in a part than a part keeps lengths of, each of its own length (n = 1, one head, so the plain form
+    is one batched product)."""
+    B, D, page, per = 12011, 64, 8, 20
+    g = gen(36)
+    lens = torch.randint(0, per * page + 1, (B,), generator=g, device="cuda", dtype=I32)
+    cache = torch.randn((2, 4096, page, 1, D), generator=g, device="cuda").to(dtype)
+    table = torch.randint(0, 4096, (B, per), generator=g, device="cuda", dtype=I32)
+    q, k, v = (torch.randn((B, 1, 1, D), generator=g, device="cuda").to(dtype) for _ in range(3))
+    op = api.TreeAttention(q, k, v, cache[0], cache[1], table, lens, lse=True)
+    out = op().outputs()
+    assert op.device_error() == 0
+    u, tiny = torch.finfo(dtype).eps / 2, torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps / 2
+    for at in range(0, B, 1001):
+        s = slice(at, at + 1001)
+        kk, vv = (torch.cat([cache[x][table[s].long()].view(-1, per * page, D), y[s, 0]], 1).double() for x, y in ((0, k), (1, v)))
+        hide = torch.arange(per * page, device="cuda") >= lens[s].view(-1, 1)
+        hide = torch.cat([hide, torch.zeros_like(hide[:, :1])], 1)
+        z = (kk @ q[s, 0].double().transpose(1, 2)).squeeze(2) / 8
+        mag = ((kk.abs() @ q[s, 0].double().abs().transpose(1, 2)).squeeze(2) / 8).masked_fill(hide, 0).amax(1, keepdim=True)
+        big = z.masked_fill(hide, 0).abs().amax(1, keepdim=True)
+        p = torch.softmax(z.masked_fill(hide, -math.inf), 1)
+        want, spread = ((p.unsqueeze(1) @ x).squeeze(1) for x in (vv, vv.abs()))
+        lse = torch.logsumexp(z.masked_fill(hide, -math.inf), 1, keepdim=True)
+        e = 2.0 ** -23 * D * mag + 2.0 ** -22 * big + 2.0 ** -21
+        T = per * page + 1
+        tol = u * want.abs() + spread * (u + 2 * e + T * 2.0 ** -24) + tiny * (1 + T * vv.abs().amax(1))
+        assert ((out["out"][s].view(-1, D).double() - want).abs() <= tol).all()
+        assert ((out["lse"][s].view(-1, 1).double() - lse).abs() <= 2 * e + T * 2.0 ** -24 + 2.0 ** -22 * lse.abs()).all()
