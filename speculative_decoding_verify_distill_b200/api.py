@@ -650,7 +650,8 @@ class _TreeOp:
 
     The calls of one object share its workspace and outputs: a call on another stream than the
     last one first waits for that stream (not while it is being captured: order captured calls
-    yourself, and give graphs that may run at the same time an object each)."""
+    yourself, give graphs that may run at the same time an object each, and keep the object as
+    long as the graph)."""
 
     _fn = ""
 
@@ -696,7 +697,8 @@ class _TreeOp:
         return self
 
     def device_error(self, stream=None) -> int:
-        """The status word of the calls so far (synchronizes)."""
+        """The status word of the calls so far; synchronizes the stream of the last call (give the one
+        that a graph was replayed on)."""
         with torch.cuda.device(self.device):
             s = self._last if stream is None else stream
             return int(lib().svd_get_device_error(self._ws, s.cuda_stream))
@@ -727,8 +729,9 @@ class TreeAttention(_TreeOp):
     ``q`` [B, n, Hq, D], ``k_new`` and ``v_new`` [B, n, Hkv, D], ``cache_k`` and ``cache_v``
     [n_pages, page_size, Hkv, D], all bf16 or all fp16; ``page_table`` [B, max_pages] and
     ``cache_len`` [B] int32.  ``parent`` [B, n] int32 gives the tree (default: a chain), ``n_nodes``
-    [B] int32 the nodes in use.  ``n = 1`` is a decode step.  Outputs: ``out`` [B, n, Hq, D] and,
-    with ``lse=True``, ``lse`` [B, n, Hq] fp32."""
+    [B] int32 the nodes in use.  ``n = 1`` is a decode step; more than 64 new tokens at once, as within
+    a prompt, are not offered.  Softmax weights are rounded to q's type for the product with V, all
+    else is fp32.  Outputs: ``out`` [B, n, Hq, D] and, with ``lse=True``, ``lse`` [B, n, Hq] fp32."""
 
     _fn = "svd_tree_attention"
 

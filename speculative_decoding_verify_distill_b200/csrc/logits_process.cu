@@ -196,8 +196,11 @@ __global__ void __launch_bounds__(kThreads, 3) logits_process_kernel(LogitsParam
     using T = typename std::conditional<F32, float, uint16_t>::type;
     constexpr int kRows = F32 ? 1 : 2;                    // rows per stage
     // Pairs per lane that are worked on at once, and whose raw logits the gradient loads ahead: as many as a dense
-    // chunk's two rows need (8 x 64 rows in bf16: 89.1 us with four, 91.6 with two), but one row of fp32 has half of
-    // them (6 x 16 rows: 25.0 us with two, 26.7 with four).
+    // chunk's two rows need, but one row of fp32 has half of them.  us with 1 / 2 / 4 in fp32:
+    //   6 x 16 rows of 128256, 700 / 4000 tokens of history   28.8 / 25.3 / 26.8,  45.4 / 40.7 / 39.7
+    //   32 x 16, 1 x 64 and 64 x 1 rows of 151936             120.1 / 120.0 / 121.5,  30.1 / 28.4 / 27.4,  35.9 / 36.1 / 36.6
+    //   4 x 8 rows of 32000                                   12.4 / 12.2 / 11.8
+    // and with 2 / 4 in bf16: 8 x 64 rows of 151936 92.9 / 90.1, 32 x 16 rows 74.6 / 73.9.
     constexpr int kAhead = F32 ? 2 : 4;
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ Tables s;

@@ -4,7 +4,11 @@
 // What bounds it: every cached key and value is read once (2 x 2 bytes x D per key head and token)
 // and serves the n * Hq / Hkv query rows of its head.  Up to about 128 rows that is less than the
 // tensor cores' rate over HBM's, so the kernel streams the cache through shared memory and does all
-// arithmetic behind it; with more rows the softmax bounds it (16 exponentials a clock and SM).
+// arithmetic behind it, until the power cap lowers the clock (1965 MHz for one request, 1335 for 128 sequences of 500
+// to 6000 tokens back to back, 1080 at 6000 each).  With more rows no unit is full: at 512 rows a key head of 64
+// elements the exponentials (16 a clock and SM) are half of the time, the tensor pipe is active in 25% of the cycles
+// and 41% of the issue slots are used; two softmax warps a scheduler, each reading S twice from TMEM, do not hide
+// one another's waits.
 //
 // Work.  An item is one sequence and key head; its keys are tiles of 128: the cached ones, then one tile of
 // the drafted nodes.  All tiles of all items form one line (with a few places for the start and end of
@@ -29,8 +33,11 @@
 // Why so (cycles a tile, heads of 128; a tile's bytes take 2800 at HBM's rate and 1965 MHz): one softmax
 // warpgroup alone took 1850 to 2200 besides its waits, of which 1024 are exponentials, and two that split the
 // columns lost as much to their exchange; one warp for all products was busy 2300, most of it with waits; one
-// warp for all loads 3200 where pages have 16 tokens.  As it is a tile takes about 1200 to 1700, so a cache
-// streams at the rate of HBM: 6000 tokens of 128 sequences at 6.8 TB/s.
+// warp for all loads 3200 where pages have 16 tokens.  As it is a tile takes about 1200 to 1700, less than its
+// bytes: 17 nodes over 6000 tokens of 128 sequences take 515 to 600 us, 5.3 to 6.2 TB/s (a copy reaches 6.5).
+//
+// The running maximum and sum are those of the online softmax (Milakov and Gimelshein, 2018); to move the reference
+// only beyond a threshold is a published refinement of it.
 //
 // Masks.  Columns behind the cache length and nodes that are not ancestors get P = 0 whatever S
 // holds.  0 * NaN would still reach O through the matrix product, so rows of V behind the length
@@ -53,8 +60,15 @@ constexpr int kCtas = 148;         // one per SM of a B200
 constexpr int kTile = 128;         // keys per tile, rows per group
 constexpr uint64_t kWaitNs = 1000000000ull;
 // Places of an item on the line besides its tiles: what its start and end cost, in tiles.  With none the parts of
-// many short items ended last: B = 32 of 1 to 4096 tokens took 94 us instead of 77, B = 128 of 500 to 6000 320
-// instead of 294 (four and six places are no better).
+// many short items ended last.  us with 0 / 2 / 3 / 4 / 6 places, 17 nodes, 32/8 heads:
+//   32 sequences of 1 to 4096 tokens, heads of 128, pages of 16     95 /  77 /  77 /  78 /  80
+//   the same, pages of 128                                          80 /  71 /  68 /  67 /  67
+//   the same, heads of 64, pages of 16                              76 /  62 /  57 /  57 /  59
+//   the same, heads of 64, pages of 128                             80 /  67 /  63 /  61 /  62
+//   128 of 500 to 6000, heads of 128, pages of 64                  336 / 320 / 313 / 308 / 304
+//   the same, heads of 64, pages of 16                             256 / 244 / 242 / 244 / 245
+//   64 of 0 to 300, heads of 128, pages of 16                       51 /  46 /  44 /  44 /  43
+//   the same, heads of 64, pages of 64                              45 /  40 /  39 /  39 /  39
 constexpr int kItemCost = 3;
 constexpr int kCombineWarps = 8;
 constexpr int kLens = 64;          // sequences of a part whose lengths are kept in shared memory
@@ -67,7 +81,8 @@ struct AttnWs {
     size_t info, ml, o, total;
 };
 // Row groups, the parts that the line is cut into at most, and CTAs (more than one per SM only where a
-// key head has more than 148 row groups).
+// key head has more than 148 row groups).  From 75 to 147 groups (9473 to 18816 rows a key head) there is one part,
+// and up to half of the SMs have nothing to do.
 __host__ __device__ inline int row_groups(int rows) { return (rows + kTile - 1) / kTile; }
 __host__ __device__ inline int max_parts(int groups) { return groups >= kCtas ? 1 : kCtas / groups; }
 inline AttnWs attn_ws(int rows, int D) {
