@@ -60,12 +60,12 @@ svd_status run_logits(const svd_logits_process_args* a, bool grad, bool aligned,
     return from_cuda(launch_logits_process(p, grad, stream));
 }
 
-// Page geometry shared by attention and append.
-bool bad_pages(int n_pages, int page_size, int max_pages, const void* ck, const void* cv,
+// Page geometry shared by attention and append (the page table of no sequences is empty).
+bool bad_pages(int B, int n_pages, int page_size, int max_pages, const void* ck, const void* cv,
                const int32_t* table, int64_t sk, int64_t sv, int64_t page_elems) {
     if (n_pages < 0 || max_pages < 0 || page_size < 1) return true;
     if (static_cast<int64_t>(max_pages) * page_size > kMaxTokens) return true;
-    if (max_pages > 0 && !table) return true;
+    if (B > 0 && max_pages > 0 && !table) return true;
     if (n_pages > 0 && (!ck || !cv)) return true;
     // pages that overlap or lie backwards make no cache
     if (n_pages > 1 && (sk < page_elems || sv < page_elems)) return true;
@@ -88,7 +88,7 @@ svd_status svd_tree_attention(const svd_tree_attention_args* a, void* ws, size_t
         return SVD_ERR_INVALID_ARG;
     if (a->dtype != SVD_BF16 && a->dtype != SVD_FP16) return SVD_ERR_INVALID_ARG;
     if (!(std::fabs(a->scale) <= 0x1p127f)) return SVD_ERR_INVALID_ARG;   // scale * log2(e) stays finite
-    if (bad_pages(a->n_pages, a->page_size, a->max_pages, a->cache_k, a->cache_v, a->page_table,
+    if (bad_pages(a->B, a->n_pages, a->page_size, a->max_pages, a->cache_k, a->cache_v, a->page_table,
                   a->page_stride_k, a->page_stride_v,
                   static_cast<int64_t>(a->page_size) * a->Hkv * a->D))
         return SVD_ERR_INVALID_ARG;
@@ -165,7 +165,7 @@ svd_status svd_cache_append(const svd_cache_append_args* a, void* ws, size_t ws_
     if (a->B < 0 || a->n < 1 || a->Hkv < 1 || a->D < 1) return SVD_ERR_INVALID_ARG;
     const int64_t row = static_cast<int64_t>(a->Hkv) * a->D;
     if (row > (1 << 24) || row % 8 != 0 || a->B > kMaxGridYZ) return SVD_ERR_UNSUPPORTED;
-    if (bad_pages(a->n_pages, a->page_size, a->max_pages, a->cache_k, a->cache_v, a->page_table,
+    if (bad_pages(a->B, a->n_pages, a->page_size, a->max_pages, a->cache_k, a->cache_v, a->page_table,
                   a->page_stride_k, a->page_stride_v, a->page_size * row))
         return SVD_ERR_INVALID_ARG;
     if (a->B == 0) return SVD_OK;

@@ -23,3 +23,13 @@ def test_attention_refuses_scales_that_overflow(L, sign):
     for scale in (2.0 ** 127 * 1.5, 3e38, 3.4e38):
         assert ctypes.c_float(scale).value < float("inf")
         assert call(scale) == 1
+
+
+def test_empty_batches_have_no_page_table(L):
+    """The page table of no sequences is an empty tensor, whose pointer is NULL."""
+    none = dict(B=0, page_table=None)
+    assert L.svd_tree_attention(_args(api.TreeAttentionArgs, ATT, none), WS, BIG, None) == 0
+    append = dict(k_new=None, v_new=None, cache_k=WS, cache_v=WS, page_stride_k=10 * 128, page_stride_v=10 * 128, n=5, Hkv=2,
+                  D=64, n_pages=9, page_size=10, max_pages=4)
+    assert L.svd_cache_append(_args(api.CacheAppendArgs, append, none), WS, BIG, None) == 0
+    assert L.svd_cache_append(_args(api.CacheAppendArgs, append, dict(B=1, page_table=None)), WS, BIG, None) == 1
