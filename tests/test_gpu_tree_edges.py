@@ -324,3 +324,61 @@ def test_attention_parts_of_many_sequences_of_differing_lengths(dtype):
         tol = u * want.abs() + spread * (u + 2 * e + T * 2.0 ** -24) + tiny * (1 + T * vv.abs().amax(1))
         assert ((out["out"][s].view(-1, D).double() - want).abs() <= tol).all()
         assert ((out["lse"][s].view(-1, 1).double() - lse).abs() <= 2 * e + T * 2.0 ** -24 + 2.0 ** -22 * lse.abs()).all()
+
+
+# ------------------------------------------------------------------------------------------
+# together
+# ------------------------------------------------------------------------------------------
+def test_a_captured_step_of_tree_decoding():
+    """Attention, logits, processing, acceptance and append as one graph, with the lengths updated in place, replayed over four
+    steps of new drafts: the tokens, lengths and cache of eager calls, bit for bit."""
+    B, n, Hq, Hkv, D, V, page, steps = 4, 12, 4, 2, 64, 512, 8, 4
+    g = gen(50)
+    emb = torch.randn((V, (2 * Hkv + Hq) * D), generator=g, device="cuda").to(BF)
+    head = (torch.randn((Hq * D, V), generator=g, device="cuda") * 0.3).to(BF)
+    parent = R.random_tree(B, n, 50).cuda()
+    drafts = torch.randint(0, 40, (steps, B, n), generator=g, device="cuda", dtype=I32)
+    prompt = torch.randn((2, B, 30, Hkv, D), generator=g, device="cuda").to(BF)
+    nn = ints([12, 7, 1, 12])
+
+    class Server:
+        def __init__(self):
+            self.cache = [torch.zeros((B * 16, page, Hkv, D), dtype=BF, device="cuda") for _ in range(2)]
+            self.table = torch.arange(B * 16, device="cuda", dtype=I32).flip(0).view(B, 16).contiguous()
+            self.lens = torch.zeros(B, dtype=I32, device="cuda")
+            api.svd_cache_append(*prompt, *self.cache, self.table, self.lens, ints([30, 9, 0, 24]), new_len=self.lens)
+            self.tok = torch.zeros((B, n), dtype=I32, device="cuda")
+
+        def step(self):
+            x = emb[self.tok.long()].view(B, n, 2 * Hkv + Hq, D)
+            q, k, v = (y.contiguous() for y in (x[:, :, 2 * Hkv:], x[:, :, :Hkv], x[:, :, Hkv:2 * Hkv]))
+            o = api.svd_tree_attention(q, k, v, *self.cache, self.table, self.lens, parent=parent, n_nodes=nn)["out"]
+            z = api.svd_logits_process(o.view(B, n, -1) @ head, node_tok=self.tok, parent=parent, argmax=True,
+                                       frequency=torch.full((B,), 0.5, device="cuda"))
+            walk = api.svd_tree_verify(self.tok, target_tok=z["argmax"], parent=parent, n_nodes=nn)
+            api.svd_cache_append(k, v, *self.cache, self.table, self.lens, walk["n_path"], path=walk["path"], new_len=self.lens)
+            return dict(walk, z=z["out"], o=o)
+
+    def draft(s, i, choice):
+        """Half of the nodes carry what the target said a step before at their parent."""
+        s.tok.copy_(drafts[i])
+        if choice is not None:
+            s.tok[:, ::2] = choice.gather(1, parent.clamp(min=0).long())[:, ::2]
+
+    eager, seen = Server(), []
+    for i in range(steps):
+        draft(eager, i, seen[-1]["target_argmax"].clamp(min=0) if seen else None)
+        seen.append({k: v.clone() for k, v in eager.step().items()})
+    server = Server()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = server.step()
+    choice = None
+    for i in range(steps):
+        draft(server, i, choice)
+        graph.replay()
+        assert same_bits(out, seen[i])
+        choice = out["target_argmax"].clamp(min=0)
+    assert torch.equal(server.lens, eager.lens)
+    assert all(torch.equal(a, b) for a, b in zip(server.cache, eager.cache))
+    assert eager.lens.tolist()[2] == steps          # a root alone is accepted in every step
